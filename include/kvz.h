@@ -387,6 +387,127 @@ kvz_status kvz_decode(const void* q, const void* K_out, const void* V_out, int64
                       size_t workspace_bytes, int32_t* d_status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Rotary positions.                                                         */
+/*                                                                          */
+/* Q, K_in, K_ctx and the decode queries are post-positional features; these */
+/* calls make them from projections.  At position p the pair (a, b) turns to */
+/*     a' = a c - b s,  b' = b c + a s,                                      */
+/* c and s being the table's cosine and sine of p * freqs[i], i < rot / 2.   */
+/* Pairs are (x[i], x[i + rot/2]), or (x[2i], x[2i + 1]) if `interleaved`;   */
+/* dims rot .. d - 1 pass through.  Products and sums are single float32     */
+/* operations; the result is rounded to bf16 once.  `inverse` turns the other */
+/* way, which is the gradient: for a loss gradient dy, the gradient of x is  */
+/* the inverse turn of dy (by the same table, so a `factor` stays a factor). */
+/*                                                                          */
+/* kvz_rotary_table: table[p][i] = factor * cos(p * freqs[i]) and            */
+/*   table[p][rot/2 + i] = factor * sin(p * freqs[i]), in float64, rounded   */
+/*   once (positions of long contexts need it).  freqs: rot / 2 doubles on   */
+/*   the device, radians per position; a scheme that scales positions for    */
+/*   long contexts is a choice of freqs and factor.  table [n_pos][rot] fp32, */
+/*   16-byte aligned.  factor finite.                                        */
+/* kvz_rotary: rows x[b][g][t] = x + b*x_sb + g*x_sg + t*x_st (strides in    */
+/*   elements, multiples of 8, not negative; d consecutive bf16 each) to the */
+/*   same rows of y, so a projection's [n][heads][d] becomes [B][G][n][d] on */
+/*   the way.  In place: y == x with equal strides; x and y must not overlap */
+/*   otherwise.  positions[b * pos_sb + t] (pos_sb 0: shared by all heads).  */
+/*   A position outside [0, n_pos) is reported (KVZ_ERR_INVALID_ARG in       */
+/*   d_status) and its rows of y are left as they were.                      */
+/* Limits: d in {64, 128}; rot a multiple of 16 in [16, d] (else             */
+/* KVZ_ERR_UNSUPPORTED); B, G <= 65535; n, n_pos <= 2^31 - 1.                */
+/* ------------------------------------------------------------------------ */
+kvz_status kvz_rotary_table(const double* freqs, int64_t n_pos, int rot, double factor, float* table,
+                            cudaStream_t stream);
+
+kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, int64_t B, int G, int64_t n,
+                      int d, const int32_t* positions, int64_t pos_sb, const float* table, int64_t n_pos,
+                      int rot, int interleaved, int inverse, void* y, int64_t y_sb, int64_t y_sg,
+                      int64_t y_st, int32_t* d_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The paged 4-bit cache (KVzip §4.2, "KV quantization"): the pruned cache   */
+/* in four bits, on pages, so that it can grow while the model answers.      */
+/*                                                                          */
+/* cache: n_pages pages of kvz_cache4_page_bytes(page_size, d) bytes (9/8 d  */
+/* per row of K and V together), 16-byte aligned.  pages [B][max_pages]      */
+/* int32: row j of head b lies in page pages[b][j / page_size], at           */
+/* j % page_size.  Entries past a head's rows may hold anything.  A page     */
+/* that several entries name may be read by all of them; calls that write    */
+/* need every page they write to be named once.  page_size: a multiple of 16 */
+/* in [16, 1024]; max_pages * page_size <= 2^30; B <= 65535; d in {64, 128}. */
+/*                                                                          */
+/* Quantisation, per row and group of 64 dims, in single float32 operations  */
+/* (ties to even): m = min x, step s = bf16((max x - m) * (1/15)) and        */
+/* code = round((x - m) * (1/s)), in 0..15; x ~= s * code + m.  A step below */
+/* 2^-126 is held as 0 (the group reads as m).  A group whose max - min is   */
+/* not finite reads as NaN.                                                  */
+/*                                                                          */
+/* Layout of a page: page_size / 16 blocks of 16 rows; a block holds, with   */
+/* NG = d / 64:                                                              */
+/*   K codes  [16 rows][4 c][NG g][2 u] 32-bit words: dims 64g + 16c + 8u +  */
+/*            0..7 as nibbles 0, 2, 4, 6, 1, 3, 5, 7 from bit 0 up, the word */
+/*            rotated left by 3                                              */
+/*   V codes  [8 row pairs][8 r][NG g][2 w][2 rows] 16-bit halves: dims 64g  */
+/*            + 8r + 4w + 0..3 of one row as nibbles 0..3 from bit 0 up      */
+/*   K scales [16 rows][NG] words: bf16 step in the low half, bf16 minimum   */
+/*            in the high half;  V scales the same.                          */
+/*                                                                          */
+/* kvz_compact_int4: for p < counts[b], row p of head b becomes row          */
+/*   idx[offsets[b] + p] of K, V [B][n_c][d] bf16 (idx, counts, offsets as   */
+/*   kvz_select writes them).  Other rows of the pages keep their bytes.     */
+/* kvz_append_int4: row counts[b] + t of head b becomes k[b][t], v[b][t], t <  */
+/*   n_new[b] (n_new NULL: T rows each; k[b][t] = k + b*k_sb + t*k_st, v and */
+/*   q[b][g][t] alike; strides in elements, multiples of 8).  With positions, */
+/*   k is turned as by kvz_rotary first (bf16, then quantised), and so is q: */
+/*   q_out [B][G][T][d] (q may be NULL, q_out then too; without positions q  */
+/*   is only laid out).  Rows of q_out at and past n_new[b] are not written. */
+/*   counts_out[b] = counts[b] + n_new[b] (optional; must not overlap        */
+/*   counts).                                                                */
+/* kvz_expand_int4: rows first[b] (NULL: 0) .. counts[b] - 1 of head b, as   */
+/*   bf16(s * code + m), to rows offsets[b], offsets[b] + 1, ... of K_out,   */
+/*   V_out [n_rows][d].  offsets [B + 1] must ascend and leave each head its */
+/*   rows: the form kvz_decode and kvz_compact use.                          */
+/* kvz_decode_int4: kvz_decode over the 4-bit cache: q [B][G][d] bf16, out   */
+/*   [B][G][d] fp32, lse2 [B][G] fp32 (optional); a head without rows gives  */
+/*   out = 0, lse2 = -inf.  1 <= G <= 8.  Workspace:                         */
+/*   kvz_decode_int4_workspace_size(G, d) bytes, 256-byte aligned; it needs  */
+/*   no initial value and is free again when the call has finished.          */
+/*                                                                          */
+/* Device-detected errors (KVZ_ERR_INVALID_ARG in d_status): a count outside */
+/* [0, max_pages * page_size] (the head is left out), a page id outside      */
+/* [0, n_pages) (rows on it are not written; reading it, the decode's output */
+/* of that head means nothing), an idx outside [0, n_c) (a row of zeros), a  */
+/* position outside the table or n_new outside [0, T] or past the table's    */
+/* last page (not appended; counts_out[b] = counts[b]), an output row past   */
+/* n_rows (the head is left out).                                            */
+/* ------------------------------------------------------------------------ */
+size_t kvz_cache4_page_bytes(int page_size, int d);
+
+kvz_status kvz_compact_int4(const void* K, const void* V, int64_t B, int64_t n_c, int d,
+                            const int32_t* idx, const int32_t* counts, const int64_t* offsets,
+                            void* cache, int64_t n_pages, int page_size, const int32_t* pages,
+                            int64_t max_pages, int32_t* d_status, cudaStream_t stream);
+
+kvz_status kvz_append_int4(const void* k, int64_t k_sb, int64_t k_st, const void* v, int64_t v_sb,
+                           int64_t v_st, const void* q, int64_t q_sb, int64_t q_sg, int64_t q_st,
+                           void* q_out, int64_t B, int G, int64_t T, int d, const int32_t* positions,
+                           int64_t pos_sb, const float* table, int64_t n_pos, int rot, int interleaved,
+                           void* cache, int64_t n_pages, int page_size, const int32_t* pages,
+                           int64_t max_pages, const int32_t* counts, const int32_t* n_new,
+                           int32_t* counts_out, int32_t* d_status, cudaStream_t stream);
+
+kvz_status kvz_expand_int4(const void* cache, int64_t n_pages, int page_size, const int32_t* pages,
+                           int64_t max_pages, const int32_t* counts, const int32_t* first,
+                           const int64_t* offsets, int64_t B, int d, void* K_out, void* V_out,
+                           int64_t n_rows, int32_t* d_status, cudaStream_t stream);
+
+size_t kvz_decode_int4_workspace_size(int G, int d);
+
+kvz_status kvz_decode_int4(const void* q, const void* cache, int64_t n_pages, int page_size,
+                           const int32_t* pages, int64_t max_pages, const int32_t* counts, int64_t B,
+                           int G, int d, float scale, float* out, float* lse2, void* workspace,
+                           size_t workspace_bytes, int32_t* d_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Chunked scoring (KVzip §3.4, "chunk-based scoring").                      */
 /*                                                                          */
 /* The context is cut into chunks of m tokens (the last one is n_c mod m     */

@@ -8,6 +8,7 @@ is missing, importing works but every call raises ``KvzLibraryError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -22,7 +23,9 @@ __all__ = [
     "kvz_select_dist_workspace_size", "kvz_select_dist_begin", "kvz_select_dist_step", "kvz_select_dist_finish",
     "kvz_compact_workspace_size", "kvz_compact", "kvz_compress_host_workspace_size", "kvz_compress_host",
     "kvz_score_chunked_workspace_size", "kvz_score_chunked", "kvz_head_score", "kvz_select_heads", "kvz_decode",
-    "kvz_select_protected", "kvz_compact_int8", "kvz_testing_compact_in_place_withhold",
+    "kvz_select_protected", "kvz_compact_int8", "kvz_rotary_freqs", "kvz_rotary_table", "kvz_rotary",
+    "kvz_cache4_page_bytes", "kvz_compact_int4", "kvz_append_int4", "kvz_expand_int4",
+    "kvz_decode_int4_workspace_size", "kvz_decode_int4", "kvz_testing_compact_in_place_withhold",
 ]
 
 PER_HEAD = 0
@@ -86,6 +89,18 @@ _SIGS = {
     "kvz_compress_host_workspace_size": (_sz, [_i64, _i32, _i64, _i64, _i32, _f64, _i32]),
     "kvz_compress_host": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _i32, _f32, _f64, _i32, _vp, _i64,
                                  _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp, _vp]),
+    "kvz_rotary_table": (_i32, [_vp, _i64, _i32, _f64, _vp, _vp]),
+    "kvz_rotary": (_i32, [_vp, _i64, _i64, _i64, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp,
+                          _i64, _i64, _i64, _vp, _vp]),
+    "kvz_cache4_page_bytes": (_sz, [_i32, _i32]),
+    "kvz_compact_int4": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "kvz_append_int4": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i32, _i64, _i32,
+                               _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp,
+                               _vp]),
+    "kvz_expand_int4": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp]),
+    "kvz_decode_int4_workspace_size": (_sz, [_i32, _i32]),
+    "kvz_decode_int4": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp,
+                               _vp]),
     "kvz_testing_compact_in_place_withhold": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _i64, _i64,
                                                      _i64, _vp, _vp]),
 }
@@ -771,6 +786,368 @@ def kvz_compact_int8(K, V, idx, counts, offsets, out_offsets=None, out_rows: Opt
                                           _ptr(out_offsets), _ptr(Kq), _ptr(Vq), _ptr(K_scale), _ptr(V_scale),
                                           _ptr(status), _stream(stream)))
     return Kq, K_scale, Vq, V_scale
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the paged 4-bit cache
+# ---------------------------------------------------------------------------
+_NULL = contextlib.nullcontext()
+
+
+def _on(fn: str, dev, stream):
+    """The context a call allocates and launches in: ``dev`` current and, with
+    a ``stream`` of the caller's, that stream current too, so that outputs and
+    scratch allocated by the call belong to the stream that uses them."""
+    if stream is None:
+        return _NULL if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device != dev:
+        raise ValueError("%s: the stream belongs to %s, the tensors to %s" % (fn, stream.device, dev))
+    return torch.cuda.stream(stream)
+
+
+def _rows_view(fn: str, name: str, t, shape):
+    """Check a bf16 tensor of rows whose last dimension is dense and whose
+    other strides keep the rows 16-byte aligned; returns those strides."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s: %s must be a torch.Tensor" % (fn, name))
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s: %s must be torch.bfloat16, got %s" % (fn, name, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s: %s must have shape %s, got %s" % (fn, name, tuple(shape), tuple(t.shape)))
+    *st, last = t.stride()
+    # the stride of a dimension of one entry is never used
+    st = [0 if n == 1 else s for n, s in zip(t.shape, st)]
+    if last != 1 or any(s % 8 for s in st) or t.data_ptr() % 16:
+        raise ValueError("%s: %s needs a dense last dimension, strides of a multiple of 8 and a 16-byte aligned base, "
+                         "got strides %s" % (fn, name, tuple(t.stride())))
+    return st
+
+
+def _span(t):
+    """The bytes [lo, hi) between a tensor's first and last element."""
+    n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+    lo = t.data_ptr()
+    return lo, lo + n * t.element_size()
+
+
+def _apart(fn: str, a_name: str, a, b_name: str, b):
+    if a is None or b is None:
+        return
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    if a0 < b1 and b0 < a1:
+        raise ValueError("%s: %s and %s must not overlap" % (fn, a_name, b_name))
+
+
+def _distinct(fn: str, name: str, t):
+    """Refuse an output whose rows share memory with one another."""
+    reach = 0
+    for s, k in sorted((s, k) for s, k in zip(t.stride(), t.shape) if k > 1):
+        if s <= reach:
+            raise ValueError("%s: rows of %s overlap (strides %s)" % (fn, name, tuple(t.stride())))
+        reach += (k - 1) * s
+
+
+def kvz_rotary_freqs(rot: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """Angles per position of the rot / 2 pairs of a head, base ** (-2i / rot)
+    radians, and the factor their cosines and sines carry; returns (freqs
+    float64 [rot / 2] on the CPU, factor) for kvz_rotary_table.
+
+    ``scaling`` stretches the positions to a longer context by
+    scaling["factor"] = s:
+
+    * {"type": "linear"}: every angle divided by s (position interpolation);
+    * {"type": "ntk"}: base * s ** (rot / (rot - 2)), so the slowest pair is
+      divided by s and the fastest kept;
+    * {"type": "yarn", "original": n}: pairs that turn more than
+      scaling["fast"] (32) times in the original n positions are kept, those
+      that turn less than scaling["slow"] (1) time are divided by s, the ones
+      between blend linearly in the pair's index; factor = 0.1 ln(s) + 1
+      unless scaling["attention"] gives it.
+    """
+    fn = "kvz_rotary_freqs"
+    rot = int(rot)
+    if rot < 16 or rot > 128 or rot % 16:
+        raise ValueError("%s: rot must be a multiple of 16 in [16, 128]" % fn)
+    base = float(base)
+    if not (base > 1.0 and math.isfinite(base)):
+        raise ValueError("%s: base must be finite and above 1" % fn)
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling is None:
+        return base ** (-2.0 * i / rot), 1.0
+    kind, s = scaling.get("type"), float(scaling.get("factor", 0.0))
+    if not (s >= 1.0 and math.isfinite(s)):
+        raise ValueError("%s: scaling needs a factor of at least 1" % fn)
+    if kind == "linear":
+        return base ** (-2.0 * i / rot) / s, 1.0
+    if kind == "ntk":
+        return (base * s ** (rot / (rot - 2.0))) ** (-2.0 * i / rot), 1.0
+    if kind == "yarn":
+        n = float(scaling.get("original", 0))
+        if not n >= 1.0:
+            raise ValueError("%s: yarn scaling needs the original length" % fn)
+        fast, slow = float(scaling.get("fast", 32.0)), float(scaling.get("slow", 1.0))
+        if not 0.0 < slow < fast:
+            raise ValueError("%s: need 0 < slow < fast" % fn)
+        f = base ** (-2.0 * i / rot)
+        # the pair (as a real index) that turns `t` times in n positions
+        at = [rot * math.log(n / (2.0 * math.pi * t)) / (2.0 * math.log(base)) for t in (fast, slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+        ramp = ((i - lo) / max(hi - lo, 0.001)).clamp(0.0, 1.0)
+        return f * (1.0 - ramp) + f / s * ramp, float(scaling.get("attention", 0.1 * math.log(s) + 1.0))
+    raise ValueError("%s: scaling type must be 'linear', 'ntk' or 'yarn'" % fn)
+
+
+def kvz_rotary_table(freqs, n_pos: int, factor: float = 1.0, table=None, stream=None):
+    """Cosines and sines of positions 0 .. n_pos - 1; returns table fp32
+    [n_pos, rot] (cosines, then sines).  freqs: float64 [rot / 2] on the
+    device, as kvz_rotary_freqs gives them."""
+    fn = "kvz_rotary_table"
+    if freqs is None:
+        raise ValueError("%s: freqs is required" % fn)
+    _req(fn, "freqs", freqs, torch.float64, ndim=1)
+    rot, n_pos = 2 * freqs.numel(), int(n_pos)
+    if n_pos < 1:
+        raise ValueError("%s: n_pos must be >= 1" % fn)
+    _req(fn, "table", table, torch.float32, shape=(n_pos, rot))
+    dev = _device(fn, freqs, table)
+    with _on(fn, dev, stream):
+        if table is None:
+            table = torch.empty((n_pos, rot), dtype=torch.float32, device=dev)
+        _check(fn, lib().kvz_rotary_table(_ptr(freqs), n_pos, rot, float(factor), _ptr(table), _stream(None)))
+    return table
+
+
+def _rotation(fn, positions, table, B, n):
+    """(pos stride, n_pos, rot) of checked positions [n] or [B, n] and table [n_pos, rot]."""
+    if positions is None or table is None:
+        raise ValueError("%s: positions and table go together" % fn)
+    _req(fn, "positions", positions, torch.int32)
+    if positions.shape != (n,) and positions.shape != (B, n):
+        raise ValueError("%s: positions must be [%d] or [%d, %d], got %s" % (fn, n, B, n, tuple(positions.shape)))
+    _req(fn, "table", table, torch.float32, ndim=2)
+    return (0 if positions.dim() == 1 else n), table.shape[0], table.shape[1]
+
+
+def kvz_rotary(x, positions, table, interleaved: bool = False, inverse: bool = False, out=None, status=None,
+               stream=None):
+    """Rotary positions of bf16 rows x [B, n, d] or [B, G, n, d]; returns out.
+
+    x may be any view with a dense last dimension (a projection's [n, heads,
+    d] transposed, say); out is dense unless given, and may be x itself (in
+    place).  positions int32 [n], or [B, n] for heads at positions of their
+    own; table as kvz_rotary_table makes it, its width being the dims that
+    turn.  ``inverse`` turns the other way: the gradient of x for a gradient
+    of out.  Nothing here is recorded for autograd."""
+    fn = "kvz_rotary"
+    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
+        raise ValueError("%s: x must be bfloat16 [B, n, d] or [B, G, n, d]" % fn)
+    shape = x.shape
+    B, G, n, d = shape if len(shape) == 4 else (shape[0], 1, shape[1], shape[2])
+    xs = _rows_view(fn, "x", x, shape)
+    pos_sb, n_pos, rot = _rotation(fn, positions, table, B, n)
+    ys = None
+    if out is not None:
+        ys = _rows_view(fn, "out", out, shape)
+        _distinct(fn, "out", out)
+        if out.data_ptr() != x.data_ptr() or ys != xs:
+            _apart(fn, "x", x, "out", out)
+    _status(fn, status)
+    dev = _device(fn, x, positions, table, out, status)
+    with _on(fn, dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            ys = out.stride()[:-1]
+        if len(shape) == 3:
+            xs, ys = (xs[0], 0, xs[1]), (ys[0], 0, ys[1])
+        _check(fn, lib().kvz_rotary(x.data_ptr(), *xs, B, G, n, d, positions.data_ptr(), pos_sb, table.data_ptr(), n_pos,
+                                    rot, int(bool(interleaved)), int(bool(inverse)), out.data_ptr(), *ys,
+                                    _ptr(status), _stream(None)))
+    return out
+
+
+def kvz_cache4_page_bytes(page_size: int, d: int) -> int:
+    """Bytes of a page of the 4-bit cache (0 for sizes it does not take)."""
+    return lib().kvz_cache4_page_bytes(int(page_size), int(d))
+
+
+def _cache4(fn, cache, pages, page_size, d=None):
+    """Check a page pool and table; returns (d, B)."""
+    if cache is None or pages is None:
+        raise ValueError("%s: cache and pages are required" % fn)
+    _req(fn, "cache", cache, torch.uint8, ndim=2)
+    _req(fn, "pages", pages, torch.int32, ndim=2)
+    if page_size < 16 or page_size > 1024 or page_size % 16:
+        raise ValueError("%s: page_size must be a multiple of 16 in [16, 1024], got %r" % (fn, page_size))
+    width = cache.shape[1]
+    if d is None:
+        d = 128 if width == page_size * 144 else 64
+    if d not in (64, 128):
+        raise ValueError("%s: head dimension must be 64 or 128, got %d" % (fn, d))
+    if width * 8 != page_size * d * 9 or cache.shape[0] < 1:
+        raise ValueError("%s: cache must be [n_pages >= 1, %d] for page_size %d and d = %d, got %s"
+                         % (fn, page_size * d * 9 // 8, page_size, d, tuple(cache.shape)))
+    if pages.shape[1] < 1:
+        raise ValueError("%s: pages must have a column at least" % fn)
+    if pages.shape[1] * page_size > 1 << 30:
+        raise ValueError("%s: a head's page table holds at most 2^30 rows" % fn)
+    return d, pages.shape[0]
+
+
+def kvz_compact_int4(K, V, idx, counts, offsets, cache, pages, page_size: int, status=None, stream=None):
+    """Kept rows into the paged 4-bit cache (KVzip §4.2 KV quantisation);
+    returns cache, whose pages now hold head b's rows 0 .. counts[b] - 1.
+
+    cache uint8 [n_pages, kvz_cache4_page_bytes(page_size, d)] and pages int32
+    [B, max_pages] are the caller's: every head needs pages for its rows, and
+    no page may be named twice."""
+    fn = "kvz_compact_int4"
+    B, n_c, d = _kv_pair(fn, K, V)
+    if idx is None or counts is None or offsets is None:
+        raise ValueError("%s: idx, counts and offsets are required" % fn)
+    _csr_args(fn, B, idx, counts, offsets)
+    page_size = int(page_size)
+    if _cache4(fn, cache, pages, page_size, d)[1] != B:
+        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
+    _status(fn, status)
+    dev = _device(fn, K, V, idx, counts, offsets, cache, pages, status)
+    with _on(fn, dev, stream):
+        _check(fn, lib().kvz_compact_int4(_ptr(K), _ptr(V), B, n_c, d, _ptr(idx), _ptr(counts), _ptr(offsets),
+                                          _ptr(cache), cache.shape[0], page_size, _ptr(pages), pages.shape[1],
+                                          _ptr(status), _stream(None)))
+    return cache
+
+
+def kvz_append_int4(k, v, cache, pages, counts, page_size: int, positions=None, table=None, interleaved: bool = False,
+                    q=None, q_out=None, n_new=None, counts_out=None, status=None, stream=None):
+    """New rows behind each head's counts[b] rows of the paged 4-bit cache;
+    returns (counts_out int32 [B], q_out).
+
+    k, v bf16 [B, T, d] (views with a dense last dimension; a decoding step is
+    T = 1).  With positions (int32 [T] or [B, T]) and a table, k is turned
+    first, and so is q, bf16 [B, G, T, d], into q_out (dense).  n_new int32
+    [B] (optional) gives how many of the T rows each head takes; the rest,
+    and their q_out rows, stay as they were.  counts is not changed:
+    counts_out holds the new lengths, for kvz_decode_int4."""
+    fn = "kvz_append_int4"
+    page_size = int(page_size)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("%s: k must be bfloat16 [B, T, d]" % fn)
+    B, T, d = k.shape
+    if _cache4(fn, cache, pages, page_size, d)[1] != B:
+        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
+    ks = _rows_view(fn, "k", k, k.shape)
+    vs = _rows_view(fn, "v", v, k.shape)
+    if counts is None:
+        raise ValueError("%s: counts is required" % fn)
+    _req(fn, "counts", counts, torch.int32, numel=B)
+    _req(fn, "n_new", n_new, torch.int32, numel=B)
+    _req(fn, "counts_out", counts_out, torch.int32, numel=B)
+    _apart(fn, "counts", counts, "counts_out", counts_out)
+    pos_sb = n_pos = rot = 0
+    if positions is not None or table is not None:
+        pos_sb, n_pos, rot = _rotation(fn, positions, table, B, T)
+    G, qs = 1, (0, 0, 0)
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != B or q.shape[2] != T or q.shape[3] != d:
+            raise ValueError("%s: q must be bfloat16 [%d, G, %d, %d]" % (fn, B, T, d))
+        G = q.shape[1]
+        qs = _rows_view(fn, "q", q, q.shape)
+        _req(fn, "q_out", q_out, torch.bfloat16, shape=q.shape)
+        _apart(fn, "q", q, "q_out", q_out)
+    elif q_out is not None:
+        raise ValueError("%s: q_out needs q" % fn)
+    _status(fn, status)
+    dev = _device(fn, k, v, cache, pages, counts, positions, table, q, q_out, n_new, counts_out, status)
+    with _on(fn, dev, stream):
+        if counts_out is None:
+            counts_out = torch.empty(B, dtype=torch.int32, device=dev)
+        if q is not None and q_out is None:
+            q_out = torch.empty((B, G, T, d), dtype=torch.bfloat16, device=dev)
+        _check(fn, lib().kvz_append_int4(
+            k.data_ptr(), *ks, v.data_ptr(), *vs, _ptr(q), *qs, _ptr(q_out), B, G, T, d, _ptr(positions), pos_sb,
+            _ptr(table), n_pos, rot, int(bool(interleaved)), cache.data_ptr(), cache.shape[0], page_size,
+            pages.data_ptr(), pages.shape[1], counts.data_ptr(), _ptr(n_new), counts_out.data_ptr(), _ptr(status),
+            _stream(None)))
+    return counts_out, q_out
+
+
+def kvz_expand_int4(cache, pages, counts, offsets, page_size: int, first=None, out_rows: Optional[int] = None,
+                    K_out=None, V_out=None, status=None, stream=None):
+    """Rows first[b] (0 when not given) .. counts[b] - 1 of each head of the
+    paged 4-bit cache as bf16 rows; returns (K_out, V_out) [rows, d], head b's
+    starting at offsets[b] (int64 [B + 1], as kvz_decode takes them).
+    ``out_rows`` sizes freshly allocated outputs."""
+    fn = "kvz_expand_int4"
+    page_size = int(page_size)
+    d, B = _cache4(fn, cache, pages, page_size)
+    if counts is None or offsets is None:
+        raise ValueError("%s: counts and offsets are required" % fn)
+    _csr_args(fn, B, None, counts, offsets)
+    _req(fn, "first", first, torch.int32, numel=B)
+    if out_rows is None and (K_out is None or V_out is None):
+        raise ValueError("%s: out_rows is required without K_out and V_out" % fn)
+    rows = K_out.shape[0] if out_rows is None else int(out_rows)
+    if rows < 0:
+        raise ValueError("%s: out_rows must not be negative" % fn)
+    for name, t in (("K_out", K_out), ("V_out", V_out)):
+        _rows_out(fn, name, t, torch.bfloat16, d, rows)
+    _apart(fn, "K_out", K_out, "V_out", V_out)
+    _status(fn, status)
+    dev = _device(fn, cache, pages, counts, first, offsets, K_out, V_out, status)
+    with _on(fn, dev, stream):
+        if K_out is None:
+            K_out = torch.empty((rows, d), dtype=torch.bfloat16, device=dev)
+        if V_out is None:
+            V_out = torch.empty((rows, d), dtype=torch.bfloat16, device=dev)
+        if rows > 0:
+            _check(fn, lib().kvz_expand_int4(
+                cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(), pages.shape[1], counts.data_ptr(),
+                _ptr(first), offsets.data_ptr(), B, d, K_out.data_ptr(), V_out.data_ptr(), rows, _ptr(status),
+                _stream(None)))
+    return K_out, V_out
+
+
+def kvz_decode_int4_workspace_size(G: int, d: int) -> int:
+    return lib().kvz_decode_int4_workspace_size(int(G), int(d))
+
+
+def kvz_decode_int4(q, cache, pages, counts, page_size: int, scale: Optional[float] = None, out=None, lse2=None,
+                    workspace=None, status=None, stream=None):
+    """One decode step of attention over the paged 4-bit cache; returns (out
+    [B, G, d] fp32, lse2 [B, G] fp32).  q is bf16 [B, G, d]; cache, pages and
+    counts are what kvz_compact_int4 and kvz_append_int4 fill."""
+    fn = "kvz_decode_int4"
+    _req(fn, "q", q, torch.bfloat16, ndim=3)
+    if q is None:
+        raise ValueError("%s: q is required" % fn)
+    B, G, d = q.shape
+    page_size = int(page_size)
+    if _cache4(fn, cache, pages, page_size, d)[1] != B:
+        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
+    if counts is None:
+        raise ValueError("%s: counts is required" % fn)
+    _req(fn, "counts", counts, torch.int32, numel=B)
+    _req(fn, "out", out, torch.float32, shape=(B, G, d))
+    _req(fn, "lse2", lse2, torch.float32, shape=(B, G))
+    _req(fn, "workspace", workspace, torch.uint8)
+    _status(fn, status)
+    dev = _device(fn, q, cache, pages, counts, out, lse2, workspace, status)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(fn, dev, stream):
+        if out is None:
+            out = torch.empty((B, G, d), dtype=torch.float32, device=dev)
+        if lse2 is None:
+            lse2 = torch.empty((B, G), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(1, lib().kvz_decode_int4_workspace_size(G, d)), dtype=torch.uint8, device=dev)
+        _check(fn, lib().kvz_decode_int4(q.data_ptr(), cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(),
+                                         pages.shape[1], counts.data_ptr(), B, G, d, scale, out.data_ptr(),
+                                         lse2.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
+                                         _stream(None)))
+    return out, lse2
 
 
 def kvz_testing_compact_in_place_withhold(K, V, idx, counts, offsets, wait_ns: int, hold_head: int,

@@ -1,0 +1,524 @@
+// Decode attention over the paged 4-bit cache.  For KV head b with n_b rows
+// and the G <= 8 grouped queries of the new token:
+//   out[b, g] = sum_j softmax_j(scale * <q_g, k_j>) v_j,
+//   k_j = s_j code_j + m_j (and v_j alike) per group of 64 dims.
+//
+// The codes are whole numbers, exact in bf16, so both products run on them
+// and the scales are applied to what comes out:
+//   <q, k_j> = sum_groups s_j <q, code_j> + m_j sum(q)
+//   out = sum_groups sum_j (p_j s_j) code_j + p_j m_j
+// A code is widened to bf16 as 16 + code (its four bits are mantissa bits 3
+// to 6 of a number in [16, 32)): one shift and one three-input logic
+// instruction per two codes.  The 16s leave with sum(q) and sum(p s), in
+// float32.  p s is split exactly into three bf16 parts (8 + 8 + 8 bits of
+// its 24), so the result keeps float32 accuracy.
+//
+// Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At that
+// rate an SM has to widen and multiply a row (both of K and V, all queries)
+// in 6 clocks, so the instructions per row bound it as much as HBM does.
+//
+// One CTA of 8 warps takes an equal share of the blocks of all heads, whatever
+// the heads' lengths (a share may end one head and begin others).  A warp
+// brings its blocks in by bulk copy through a ring of its own, one copy per
+// 16-row block, and keeps a running (reference, sum, output) per query; the
+// warps merge in shared memory at the end of each head's part.  A head that
+// several CTAs read leaves one partial per CTA, which a second launch joins
+// in order: no atomics, and identical inputs give identical results.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kvz.h"
+#include "kvz_cache4.cuh"
+#include "kvz_internal.h"
+#include "kvz_sm100.cuh"
+
+namespace kvz {
+
+namespace {
+
+constexpr int kD4Warps = 8;
+constexpr int kD4Threads = kD4Warps * 32;
+constexpr int kD4Stages = 4;
+constexpr int kD4MinBlocks = kD4Warps;                        // a CTA's share is at least a block per warp
+constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
+constexpr float kD4Slack = 8.0f;                              // log2 by which a logit may pass the reference
+
+template <int D>
+struct D4 {
+  static constexpr int KS = D / 16;                           // k-steps of Q K^T
+  static constexpr int MT = D / 16;                           // 16-dim tiles of the output
+  static constexpr int RING = kD4Warps * kD4Stages * C4<D>::BLOCK;
+  static constexpr int O_OFF = RING;                          // float [warps][8][D]
+  static constexpr int SMEM = RING + kD4Warps * 8 * D * 4;
+};
+static_assert(D4<128>::SMEM <= 107 * 1024, "two CTAs per SM");
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two codes of a word, in bits 3..6 of its halves after the shift, as bf16 16 + code.
+__device__ __forceinline__ uint32_t wide2(uint32_t w) { return (w & 0x00780078u) | 0x41804180u; }
+
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+__device__ __forceinline__ int64_t blocks_of(int c, int64_t cap) {
+  return c < 0 || c > cap ? 0 : (c + kC4Rows - 1) / kC4Rows;
+}
+
+// Sum over the CTA, in every thread.
+__device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* s_red) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t t = 0;
+  for (int i = 0; i < kD4Warps; ++i) t += s_red[i];
+  __syncthreads();
+  return t;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) {
+  using L = C4<D>;
+  using S = D4<D>;
+  constexpr int NG = L::NG;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kD4Warps * kD4Stages];
+  __shared__ int s_abort;
+  __shared__ int s_cnt[kD4Counts];
+  __shared__ int64_t s_red[kD4Warps];
+  __shared__ int64_t s_find[2];                               // head that holds the first block, its first block
+  __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int G = p.G;
+  volatile int* abort_flag = &s_abort;
+
+  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
+  if (tid == 0) s_abort = 0;
+  fence_mbar_init();
+
+  // ---- this CTA's share [u0, u1) of all heads' blocks
+  int64_t mine = 0;
+  for (int64_t b = tid; b < p.B; b += kD4Threads) {
+    const int n = p.counts[b];
+    if (b < kD4Counts) s_cnt[b] = n;
+    mine += blocks_of(n, p.cap);
+  }
+  const int64_t total = cta_sum(mine, s_red);
+  int64_t quota = (total + kD4Workers - 1) / kD4Workers;
+  quota = quota < kD4MinBlocks ? kD4MinBlocks : quota;
+  const int64_t u0 = blockIdx.x * quota;
+  const int64_t u1 = u0 + quota < total ? u0 + quota : total;
+  auto count_of = [&](int64_t b) -> int { return b < kD4Counts ? s_cnt[b] : p.counts[b]; };
+
+  // heads without rows get their outputs here, heads with a bad count a report
+  for (int64_t b = blockIdx.x; b < p.B; b += kD4Workers) {
+    const int n = count_of(b);
+    if (n == 0) {
+      for (int e = tid; e < G * D; e += kD4Threads) p.out[b * G * D + e] = 0.0f;
+      if (p.lse2 != nullptr && tid < G) p.lse2[b * G + tid] = -INFINITY;
+    } else if ((n < 0 || n > p.cap) && tid == 0) {
+      report(p.status, KVZ_ERR_INVALID_ARG);
+    }
+  }
+  if (u0 >= u1) {
+    if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  // the head that holds block u0: scan the heads' block counts, a CTA's width at a time
+  {
+    int64_t carry = 0;
+    for (int64_t b0 = 0; b0 < p.B; b0 += kD4Threads) {
+      const int64_t b = b0 + tid;
+      const int64_t n = b < p.B ? blocks_of(count_of(b), p.cap) : 0;
+      int64_t inc = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFullMask, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) s_red[warp] = inc;
+      __syncthreads();
+      int64_t before = carry, all = 0;
+      for (int i = 0; i < kD4Warps; ++i) {
+        if (i < warp) before += s_red[i];
+        all += s_red[i];
+      }
+      const int64_t start = before + inc - n;
+      if (u0 >= start && u0 < start + n) {
+        s_find[0] = b;
+        s_find[1] = start;
+      }
+      carry += all;
+      __syncthreads();
+      if (carry > u0) break;                                  // uniform
+    }
+  }
+  int64_t b = s_find[0], start = s_find[1];
+
+  uint64_t* bar = full + warp * kD4Stages;
+  uint8_t* ring = smem + warp * (kD4Stages * L::BLOCK);
+  float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
+  uint32_t used = 0;                                          // blocks this warp has taken from its ring
+  int4 cont = make_int4(-1, 0, 0, 0);
+
+  for (;;) {
+    const int count = count_of(b);
+    const int64_t n_blk = blocks_of(count, p.cap);
+    const int a0 = static_cast<int>(u0 > start ? u0 - start : 0);
+    const int a1 = static_cast<int>(u1 - start < n_blk ? u1 - start : n_blk);
+    const int n = a1 - a0 > warp ? (a1 - a0 - warp + kD4Warps - 1) / kD4Warps : 0;   // this warp's blocks
+
+    // lane 0 keeps the ring full: block i of the warp is block a0 + warp + 8 i of the head
+    const int32_t* const row_pages = p.pg.pages + b * p.pg.max_pages;
+    auto page_id = [&](int i) -> int {
+      return i < n ? __ldg(row_pages + page_of(p.pg, static_cast<uint32_t>(a0 + warp + kD4Warps * i))) : 0;
+    };
+    auto issue = [&](int i, uint32_t ahead, int id) {          // `ahead`: how far past the block now taken
+      const uint32_t blk = static_cast<uint32_t>(a0 + warp + kD4Warps * i);
+      if (id < 0 || id >= p.pg.n_pages) {                     // reported; page 0 stands in, so the read stays inside
+        report(p.status, KVZ_ERR_INVALID_ARG);
+        id = 0;
+      }
+      const uint32_t st = (used + ahead) % kD4Stages;
+      mbar_arrive_expect_tx(&bar[st], L::BLOCK);
+      bulk_load(ring + st * L::BLOCK,
+                p.pg.cache + (static_cast<int64_t>(id) * p.pg.blocks + (blk - page_of(p.pg, blk) * p.pg.blocks)) *
+                                 L::BLOCK,
+                L::BLOCK, &bar[st]);
+    };
+    __syncthreads();                                          // barriers are initialised; s_o of the last part is read
+    int id_next = 0;
+    if (lane == 0) {
+      int id[kD4Stages];
+#pragma unroll
+      for (int i = 0; i < kD4Stages; ++i) id[i] = page_id(i);
+      id_next = page_id(kD4Stages);
+#pragma unroll
+      for (int i = 0; i < kD4Stages; ++i)
+        if (i < n) issue(i, i, id[i]);
+    }
+
+    // Q fragments (rows = queries; rows >= G are zero) and -16 sum(q), sum(q) per group
+    uint32_t qa[S::KS][2];
+    float qs[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < G) v = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
+        qa[4 * g + 2 * u][0] = v.x, qa[4 * g + 2 * u][1] = v.y;
+        qa[4 * g + 2 * u + 1][0] = v.z, qa[4 * g + 2 * u + 1][1] = v.w;
+        sum += ((bf_lo(v.x) + bf_hi(v.x)) + (bf_lo(v.y) + bf_hi(v.y))) +
+               ((bf_lo(v.z) + bf_hi(v.z)) + (bf_lo(v.w) + bf_hi(v.w)));
+      }
+      sum += __shfl_xor_sync(kFullMask, sum, 1);
+      sum += __shfl_xor_sync(kFullMask, sum, 2);
+      qs[g] = sum;
+    }
+
+    float o[S::MT][4];                                        // out^T tiles: dims x queries 2c, 2c + 1
+#pragma unroll
+    for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+    float m_ref = -INFINITY, thr = -INFINITY;                 // of query r
+    float l_run = 0.0f;                                       // of query r, this lane's keys
+    float om[NG];                                             // sum of p (m - 16 s), the same
+#pragma unroll
+    for (int g = 0; g < NG; ++g) om[g] = 0.0f;
+
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t st = used % kD4Stages;
+      ok = mbar_wait_warp(&bar[st], (used / kD4Stages) & 1u, abort_flag, p.status);
+      if (!ok) break;                                         // warp-uniform
+      const uint8_t* blk = ring + st * L::BLOCK;
+
+      // ---- scores of query r and keys 8t + 2c + e of the block
+      float x[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t kw[2 * NG], kp[2 * NG];
+        lds_words(blk + (8 * t + r) * (D / 2) + c * (8 * NG), kw);
+        lds_words(blk + L::KS_OFF + (8 * t + 2 * c) * (4 * NG), kp);
+        x[t][0] = x[t][1] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float acc[4];
+          const float init = -16.0f * qs[g];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t w = kw[2 * g + u];
+            const uint32_t(&q0)[2] = qa[4 * g + 2 * u], (&q1)[2] = qa[4 * g + 2 * u + 1];
+            if (u == 0)
+              mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2(w), wide2(w >> 4), init, init, 0.0f, 0.0f);
+            else
+              mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2(w), wide2(w >> 4), acc[0], acc[1], acc[2], acc[3]);
+            mma_16816(acc, q1[0], 0u, q1[1], 0u, wide2(w >> 8), wide2(__funnelshift_r(w, w, 12)), acc[0], acc[1],
+                      acc[2], acc[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t sm = kp[e * NG + g];
+            x[t][e] = fmaf(bf_lo(sm), acc[e], fmaf(bf_hi(sm), qs[g], x[t][e]));
+          }
+        }
+      }
+      uint32_t vp[2][2 * NG];                                 // V scales of the same keys
+#pragma unroll
+      for (int t = 0; t < 2; ++t) lds_words(blk + L::VS_OFF + (8 * t + 2 * c) * (4 * NG), vp[t]);
+      const int rows = count - (a0 + warp + kD4Warps * i) * kC4Rows;
+      if (rows < kC4Rows) {                                   // the head's last block: rows past its end do not count,
+#pragma unroll                                                // whatever the page holds there
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (8 * t + 2 * c + e >= rows) {
+              x[t][e] = -INFINITY;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) vp[t][e * NG + g] = 0u;
+            }
+      }
+      // ---- softmax against a reference that moves only when a logit passes it by 2^8
+      const float xm = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+      if (__any_sync(kFullMask, xm > thr)) {
+        float mx = fmaxf(xm, __shfl_xor_sync(kFullMask, xm, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+        const bool up = mx > thr;
+        const float mn = up ? mx * p.c2 : m_ref;
+        const float alpha = up ? ex2(m_ref - mn) : 1.0f;      // 0 the first time
+        if (up) {
+          m_ref = mn;
+          thr = (mn + kD4Slack) / p.c2;
+          l_run *= alpha;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) om[g] *= alpha;
+        }
+        const float al0 = __shfl_sync(kFullMask, alpha, 8 * c), al1 = __shfl_sync(kFullMask, alpha, 8 * c + 4);
+#pragma unroll
+        for (int t = 0; t < S::MT; ++t) {
+          o[t][0] *= al0, o[t][1] *= al1;
+          o[t][2] *= al0, o[t][3] *= al1;
+        }
+      }
+      float pr[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          pr[t][e] = ex2(fmaf(x[t][e], p.c2, -m_ref));
+          l_run += pr[t][e];
+        }
+
+      // ---- out^T += V^T (p s)
+      uint32_t vw[2][2 * NG];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) lds_words(blk + L::V_OFF + (4 * t + c) * D + r * (8 * NG), vw[t]);
+      __syncwarp();
+      if (lane == 0 && i + kD4Stages < n) {                   // the stage is in registers: refill it
+        const int id = id_next;
+        id_next = page_id(i + kD4Stages + 1);
+        issue(i + kD4Stages, kD4Stages, id);
+      }
+      ++used;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t part[3][2];                                  // [hi, mid, lo][t]
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float w0, w1;
+          {
+            const float s0 = bf_lo(vp[t][g]), s1 = bf_lo(vp[t][NG + g]);
+            w0 = pr[t][0] * s0;
+            w1 = pr[t][1] * s1;
+            om[g] = fmaf(pr[t][0], fmaf(-16.0f, s0, bf_hi(vp[t][g])), om[g]);
+            om[g] = fmaf(pr[t][1], fmaf(-16.0f, s1, bf_hi(vp[t][NG + g])), om[g]);
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {                       // truncated to 8 bits each; what is left is exact
+            part[k][t] = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+            if (k < 2) {
+              w0 -= __uint_as_float(__float_as_uint(w0) & 0xFFFF0000u);
+              w1 -= __uint_as_float(__float_as_uint(w1) & 0xFFFF0000u);
+            }
+          }
+        }
+#pragma unroll
+        for (int wl = 0; wl < 2; ++wl) {
+          const uint32_t y0 = vw[0][2 * g + wl], y1 = vw[1][2 * g + wl];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {                       // dims 64g + 8r + 4wl + 2h, + 1
+            const uint32_t a00 = wide2(h == 0 ? y0 << 3 : y0 >> 5), a10 = wide2(h == 0 ? y0 >> 1 : y0 >> 9);
+            const uint32_t a01 = wide2(h == 0 ? y1 << 3 : y1 >> 5), a11 = wide2(h == 0 ? y1 >> 1 : y1 >> 9);
+            float(&d)[4] = o[4 * g + 2 * wl + h];
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              mma_16816(d, a00, a10, a01, a11, part[k][0], part[k][1], d[0], d[1], d[2], d[3]);
+          }
+        }
+      }
+    }
+    if (!ok) {                                                // a wait expired: let this warp's own copies land
+      if (lane == 0)
+        for (int i = 0; i < kD4Stages; ++i) mbar_wait_for(&bar[(used + i) % kD4Stages], ((used + i) / kD4Stages) & 1u,
+                                                          20000000ull);
+    }
+
+    // ---- this head's part is read: the warps' states to shared memory
+    l_run += __shfl_xor_sync(kFullMask, l_run, 1);
+    l_run += __shfl_xor_sync(kFullMask, l_run, 2);
+    if (c == 0) {
+      s_m[warp][r] = m_ref;
+      s_l[warp][r] = l_run;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float v = om[g];
+      v += __shfl_xor_sync(kFullMask, v, 1);
+      v += __shfl_xor_sync(kFullMask, v, 2);
+      const float v0 = __shfl_sync(kFullMask, v, 8 * c), v1 = __shfl_sync(kFullMask, v, 8 * c + 4);
+      float* d0 = s_o + (warp * 8 + 2 * c) * D + 64 * g + 8 * r;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float(&x0)[4] = o[4 * g + 2 * h], (&x1)[4] = o[4 * g + 2 * h + 1];
+        *reinterpret_cast<float4*>(d0 + 4 * h) = make_float4(x0[0] + v0, x0[2] + v0, x1[0] + v0, x1[2] + v0);
+        *reinterpret_cast<float4*>(d0 + D + 4 * h) = make_float4(x0[1] + v1, x0[3] + v1, x1[1] + v1, x1[3] + v1);
+      }
+    }
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {                                             // uniform: the output of this share is not written
+      if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    const bool whole = a0 == 0 && a1 == n_blk, past = a1 < n_blk;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (past ? 1 : 0);
+    for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
+      const int g = 4 * e4 / D;
+      float M = -INFINITY, Ls = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kD4Warps; ++w) M = fmaxf(M, s_m[w][g]);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kD4Warps; ++w) {
+        const float mw = s_m[w][g], lw = s_l[w][g];
+        const bool none = mw == -INFINITY && lw == 0.0f;      // the warp had no block
+        const float wgt = none ? 0.0f : exp2f(mw - M);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + w * 8 * D + 4 * e4);
+        Ls = fmaf(lw, wgt, Ls);
+        acc.x = fmaf(v.x, wgt, acc.x), acc.y = fmaf(v.y, wgt, acc.y);
+        acc.z = fmaf(v.z, wgt, acc.z), acc.w = fmaf(v.w, wgt, acc.w);
+      }
+      if (whole) {
+        reinterpret_cast<float4*>(p.out + b * G * D)[e4] =
+            make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + g] = M + log2f(Ls);
+      } else {
+        reinterpret_cast<float4*>(p.part_o + slot * G * D)[e4] = acc;
+        if ((4 * e4) % D == 0) p.part_ml[slot * 8 + g] = make_float2(M, Ls);
+      }
+    }
+    if (a0 == 0 && past)                                      // this CTA begins the head, others go on with it
+      cont = make_int4(static_cast<int>(b), static_cast<int>((start + n_blk - 1) / quota), 0, 0);
+    if (start + n_blk >= u1) break;
+    start += n_blk;
+    do ++b; while (blocks_of(count_of(b), p.cap) == 0);       // there is a next one: u1 <= total
+  }
+  if (tid == 0) p.cont[blockIdx.x] = cont;
+}
+
+// The heads that CTA blockIdx.x began and others went on with: their partials
+// (reference m, sum l, output o) join as M = max m, sum l 2^(m - M), sum o
+// 2^(m - M), in the CTAs' order.
+template <int D>
+__global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
+  constexpr int C = D / 4, RS = kD4Threads / C;               // float4 columns, partials read side by side
+  __shared__ float s_w[kD4Workers];
+  __shared__ float s_red[kD4Warps], s_red2[kD4Warps];
+  __shared__ float4 s_acc[kD4Threads];
+  const int first = blockIdx.x, tid = threadIdx.x, G = p.G;
+  const int4 cont = p.cont[first];
+  if (cont.x < 0) return;
+  const int np = cont.y - first + 1;                          // CTAs first .. last: all but the last run past their range
+  auto slot = [&](int i) -> int64_t { return 2 * static_cast<int64_t>(first + i) + (i + 1 < np ? 1 : 0); };
+  for (int g = blockIdx.y; g < G; g += gridDim.y) {
+    float M = -INFINITY, Ls = 0.0f;
+    for (int i = tid; i < np; i += kD4Threads) M = fmaxf(M, p.part_ml[slot(i) * 8 + g].x);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    __syncthreads();
+    if ((tid & 31) == 0) s_red[tid >> 5] = M;
+    __syncthreads();
+    for (int i = 0; i < kD4Warps; ++i) M = fmaxf(M, s_red[i]);
+    for (int i = tid; i < np; i += kD4Threads) {
+      const float2 ml = p.part_ml[slot(i) * 8 + g];
+      const float w = exp2f(ml.x - M);
+      s_w[i] = w;
+      Ls = fmaf(ml.y, w, Ls);
+    }
+    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFullMask, Ls, o);
+    if ((tid & 31) == 0) s_red2[tid >> 5] = Ls;
+    __syncthreads();
+    Ls = 0.0f;
+    for (int i = 0; i < kD4Warps; ++i) Ls += s_red2[i];
+    const int col = tid % C, lanep = tid / C;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = lanep; i < np; i += RS) {
+      const float4 v = reinterpret_cast<const float4*>(p.part_o + (slot(i) * G + g) * D)[col];
+      const float w = s_w[i];
+      acc.x = fmaf(v.x, w, acc.x), acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z), acc.w = fmaf(v.w, w, acc.w);
+    }
+    s_acc[tid] = acc;
+    __syncthreads();
+    if (tid < C) {
+      for (int i = 1; i < RS; ++i) {
+        const float4 v = s_acc[i * C + tid];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      const int64_t at = static_cast<int64_t>(cont.x) * G + g;
+      reinterpret_cast<float4*>(p.out + at * D)[tid] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+      if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = M + log2f(Ls);
+    }
+    __syncthreads();
+  }
+}
+
+template <int D>
+cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
+  cudaError_t e = smem_limit_once<decode_int4_kernel<D>>(D4<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  decode_int4_kernel<D><<<kD4Workers, kD4Threads, D4<D>::SMEM, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  merge_int4_kernel<D><<<dim3(kD4Workers, static_cast<unsigned>(a.G)), kD4Threads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_int4(int d, const Dec4Args& a, cudaStream_t stream) {
+  return d == 128 ? launch_decode4<128>(a, stream) : launch_decode4<64>(a, stream);
+}
+
+}  // namespace kvz

@@ -1,0 +1,159 @@
+// The paged 4-bit cache: its layout, and the device helpers that the kernels
+// writing and reading it share.
+//
+// A page holds page_size rows of one head as page_size / 16 blocks.  A block
+// of 16 rows is one contiguous record, so it moves as a single bulk copy, and
+// its codes lie in the order in which the attention's matrix instructions
+// take them: a lane reads its share of 16 keys as whole 16-byte words and
+// widens it in registers, with nothing to transpose.  With NG = D / 64:
+//   K codes   [16 rows][4 c][NG g][2 u] words: dims 64g + 16c + 8u + 0..7 as
+//             nibbles 0, 2, 4, 6, 1, 3, 5, 7, the word rotated left by 3
+//   V codes   [8 row pairs][8 r][NG g][2 w][2 rows] halves: dims 64g + 8r +
+//             4w + 0..3 of one row as nibbles 0, 1, 2, 3
+//   K scales  [16 rows][NG] words: bf16 step (low half), bf16 minimum (high)
+//   V scales  the same
+// The two rows of a V pair are the two halves of a word, so a row can be
+// written without reading its neighbour's.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kvz.h"
+#include "kvz_internal.h"
+#include "kvz_sm100.cuh"
+
+namespace kvz {
+
+constexpr int kC4Rows = 16;                                   // rows of a block
+constexpr uint32_t kFullMask = 0xffffffffu;
+
+template <int D>
+struct C4 {
+  static constexpr int NG = D / 64;                           // groups of 64 dims, one (step, minimum) each
+  static constexpr int V_OFF = 8 * D;
+  static constexpr int KS_OFF = 16 * D;
+  static constexpr int VS_OFF = 17 * D;
+  static constexpr int BLOCK = 18 * D;                        // bytes of a block
+  static constexpr int LPR = D / 8;                           // lanes that hold a row, 8 dims each
+};
+
+// Block blk of head b: its address, or null (and a report) for a page id
+// outside the pool.  The caller has checked blk against the table's width.
+template <int D>
+__device__ __forceinline__ uint8_t* block_at(const Pages4& pg, int64_t b, uint32_t blk, int32_t* status) {
+  const uint32_t pi = page_of(pg, blk);
+  const int32_t id = __ldg(pg.pages + b * pg.max_pages + pi);
+  if (id < 0 || id >= pg.n_pages) {
+    report(status, KVZ_ERR_INVALID_ARG);
+    return nullptr;
+  }
+  return pg.cache + (static_cast<int64_t>(id) * pg.blocks + (blk - pi * pg.blocks)) * C4<D>::BLOCK;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Codes and scale word of the 8 consecutive values in x; the group of 64 is
+// the 8 lanes that differ in the low three bits (all lanes take part).  With
+// m = min, r = max - min: step s = bf16(r * (1/15)), code = round((x - m) *
+// (1/s)), every step one IEEE float32 operation, ties to even.  (r * (1/15)
+// rounded to bf16 is at least r/15 * (1 - 2^-8), so a code is at most 15.06
+// before it is rounded.)  A step below 2^-126 is held as 0, with codes 0: its
+// reciprocal leaves float32, and the whole group is within 2^-122 of m.  A
+// group whose range is not finite (a NaN, an infinity or a range past
+// float32) is held as step NaN, so reading it gives NaN.
+// code[i] = 0x4B400000 + the code of value i.
+__device__ __forceinline__ bool quantise8(const uint4& x, uint32_t (&code)[8], uint32_t& sm) {
+  const uint32_t lo2 = min_nan2(min_nan2(x.x, x.y), min_nan2(x.z, x.w));
+  const uint32_t hi2 = max_nan2(max_nan2(x.x, x.y), max_nan2(x.z, x.w));
+  // (min, -max) in one word, so that one minimum over the lanes serves both
+  uint32_t v = __byte_perm(min_nan2(lo2, lo2 >> 16), max_nan2(hi2, hi2 >> 16) ^ 0x8000u, 0x5410);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v = min_nan2(v, __shfl_xor_sync(kFullMask, v, o));
+  const float m = bf_lo(v), r = __fadd_rn(__uint_as_float((v ^ 0x80000000u) & 0xFFFF0000u), -m);
+  const bool fine = r < INFINITY;
+  float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(r, 1.0f / 15.0f)));
+  s = s < 0x1p-126f ? 0.0f : s;
+  const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  sm = fine ? ((__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u)) : 0x00007FC0u;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    code[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(bf_lo(w[i]), m), inv), 12582912.0f));
+    code[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(bf_hi(w[i]), m), inv), 12582912.0f));
+  }
+  return fine;
+}
+
+// Sum of code[i] << shift with the constant 0x4B400000 parts taken out (the
+// arithmetic is modulo 2^32, so they cancel exactly).
+constexpr uint32_t kCodeBias = 0x4B400000u;
+
+// Write one row pair's K codes: lane l of the row's D / 8 lanes holds dims
+// 8l .. 8l + 7, which are one word of the row.
+template <int D>
+__device__ __forceinline__ void store_k(uint8_t* blk, int row, int l, const uint32_t (&code)[8], bool fine,
+                                        uint32_t sm) {
+  using L = C4<D>;
+  constexpr uint32_t bias = kCodeBias * 0x11111111u;
+  uint32_t w = code[0] + (code[1] << 16) + (code[2] << 4) + (code[3] << 20) + (code[4] << 8) + (code[5] << 24) +
+               (code[6] << 12) + (code[7] << 28) - bias;
+  w = fine ? w : 0u;
+  w = __funnelshift_l(w, w, 3);
+  const int g = l / 8, c = (l % 8) / 2, u = l % 2;
+  *reinterpret_cast<uint32_t*>(blk + row * (D / 2) + (c * L::NG * 2 + g * 2 + u) * 4) = w;
+  if (l % 8 == 0) *reinterpret_cast<uint32_t*>(blk + L::KS_OFF + (row * L::NG + g) * 4) = sm;
+}
+
+// The same for V.  Lanes l and l ^ LPR hold the same dims of the pair's even
+// and odd row; where both rows are written, each lane stores one whole word
+// (all lanes take part in the exchange), else a written row's two halves.
+template <int D>
+__device__ __forceinline__ void store_v(uint8_t* blk, int row, int l, const uint32_t (&code)[8], bool fine,
+                                        uint32_t sm, bool write) {
+  using L = C4<D>;
+  constexpr uint32_t bias = kCodeBias * 0x1111u;
+  uint32_t h0 = (code[0] + (code[1] << 4) + (code[2] << 8) + (code[3] << 12) - bias) & 0xFFFFu;
+  uint32_t h1 = (code[4] + (code[5] << 4) + (code[6] << 8) + (code[7] << 12) - bias) & 0xFFFFu;
+  h0 = fine ? h0 : 0u;
+  h1 = fine ? h1 : 0u;
+  const bool odd = (row & 1) != 0;
+  const uint32_t got = __shfl_xor_sync(kFullMask, (odd ? h0 : h1) | (write ? 0x10000u : 0u), L::LPR);
+  const bool both = write && (got & 0x10000u) != 0;
+  const int g = l / 8, r = l % 8;
+  uint8_t* at = blk + L::V_OFF + (row >> 1) * D + (r * L::NG + g) * 8;       // two words: dims 0..3, 4..7
+  if (both) {
+    const uint32_t w = odd ? ((got & 0xFFFFu) | (h1 << 16)) : (h0 | (got << 16));
+    *reinterpret_cast<uint32_t*>(at + (odd ? 4 : 0)) = w;
+  } else if (write) {
+    *reinterpret_cast<uint16_t*>(at + (odd ? 2 : 0)) = static_cast<uint16_t>(h0);
+    *reinterpret_cast<uint16_t*>(at + 4 + (odd ? 2 : 0)) = static_cast<uint16_t>(h1);
+  }
+  if (write && l % 8 == 0) *reinterpret_cast<uint32_t*>(blk + L::VS_OFF + (row * L::NG + g) * 4) = sm;
+}
+
+// s * code + m of the code in the low four bits of w (one rounding: s * code
+// is exact in float32).
+__device__ __forceinline__ float widen4(uint32_t w, float s, float m) {
+  return __fmaf_rn(s, __uint_as_float((w & 15u) | 0x4B000000u) - 8388608.0f, m);
+}
+
+}  // namespace kvz

@@ -157,4 +157,88 @@ cudaError_t launch_compact_int8(const void* K, const void* V, int64_t B, int64_t
                                 int8_t* Kq, int8_t* Vq, float* K_scale, float* V_scale, int32_t* status,
                                 cudaStream_t stream);
 
+// The paged 4-bit cache (layout in kvz_cache4.cuh): `cache` is a pool of
+// n_pages pages, pages[b][i] the page of rows [i * page_size, (i + 1) *
+// page_size) of head b.
+struct Pages4 {
+  uint8_t* cache;
+  int64_t n_pages;
+  const int32_t* pages;                     // [B][max_pages]
+  int64_t max_pages;
+  uint32_t blocks;                          // 16-row blocks per page
+  uint32_t inv;                             // floor(2^32 / blocks) + 1 (0 when blocks == 1)
+};
+// blk / blocks for blk < 2^26 and blocks <= 64: inv * blocks exceeds 2^32 by
+// at most 64, so the product is off by less than 2^32 / blocks.
+__host__ __device__ inline uint32_t page_of(const Pages4& p, uint32_t blk) {
+  return p.inv == 0 ? blk : static_cast<uint32_t>((static_cast<uint64_t>(blk) * p.inv) >> 32);
+}
+
+// Kept rows of K, V [B][n_c][d] into the 4-bit cache.
+cudaError_t launch_compact_int4(const void* K, const void* V, int64_t B, int64_t n_c, int d, const int32_t* idx,
+                                const int32_t* counts, const int64_t* offsets, const Pages4& pg, int32_t* status,
+                                cudaStream_t stream);
+// Rows first[b] .. counts[b] of the 4-bit cache as bf16 rows from offsets[b] on.
+cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const int32_t* first, const int64_t* offsets,
+                               int64_t B, int d, void* K_out, void* V_out, int64_t n_rows, int32_t* status,
+                               cudaStream_t stream);
+
+// Rotary positions.  Strides in elements; pos_sb is 0 for positions shared by all heads.
+struct RotArgs {
+  const int32_t* pos;                       // null: no rotation
+  int64_t pos_sb;
+  const float* table;                       // [n_pos][rot]: rot/2 cosines, rot/2 sines
+  int64_t n_pos;
+  int rot, interleaved, inverse;
+};
+struct RotaryArgs {
+  const uint16_t* x;
+  int64_t x_sb, x_sg, x_st;
+  uint16_t* y;
+  int64_t y_sb, y_sg, y_st;
+  int64_t B, T;
+  int G;
+  RotArgs rot;
+  int32_t* status;
+};
+cudaError_t launch_rotary(int d, const RotaryArgs& a, cudaStream_t stream);
+cudaError_t launch_rotary_table(const double* freqs, int64_t n_pos, int rot, double factor, float* table,
+                                cudaStream_t stream);
+
+// New rows behind each head's counts[b] rows of the 4-bit cache.
+struct Append4Args {
+  const uint16_t *k, *v, *q;                // q may be null
+  int64_t k_sb, k_st, v_sb, v_st, q_sb, q_sg, q_st;
+  uint16_t* q_out;                          // [B][G][T][d]
+  int64_t B, T;
+  int G;
+  RotArgs rot;
+  Pages4 pg;
+  const int32_t* counts;
+  const int32_t* n_new;                     // null: T rows each
+  int32_t* counts_out;                      // may be null
+  int32_t* status;
+};
+cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream);
+
+// Decode attention over the 4-bit cache: kD4Workers CTAs share the heads' 16-row
+// blocks evenly; the heads that more than one CTA read are merged.
+constexpr int kD4Workers = 148 * 2;         // two CTAs per SM
+struct Dec4Args {
+  Pages4 pg;
+  int64_t B;
+  int G;
+  int64_t cap;                              // rows a head's page table can hold
+  float c2;                                 // scale * log2(e)
+  const uint16_t* q;                        // bf16 [B][G][d]
+  const int32_t* counts;
+  float* out;                               // [B][G][d]
+  float* lse2;                              // [B][G], may be null
+  int4* cont;                               // [kD4Workers] the head that runs past each CTA's range
+  float2* part_ml;                          // [2 * kD4Workers][8] partial (reference, sum)
+  float* part_o;                            // [2 * kD4Workers][G][d]
+  int32_t* status;
+};
+cudaError_t launch_decode_int4(int d, const Dec4Args& a, cudaStream_t stream);
+
 }  // namespace kvz

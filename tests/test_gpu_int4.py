@@ -1,0 +1,571 @@
+"""GPU parity of the paged 4-bit cache.  What is written (codes, scales and
+their places) is bit for bit the oracle's, which takes the same float32 steps;
+reading back is one float32 sum rounded to bf16, also bit for bit; attention
+is held to the bound that its float32 steps allow (decode_bound), against
+float64 over the values that the bytes stand for."""
+import numpy as np
+import pytest
+import torch
+
+from kvz_testutil import bits, f64
+from oracle import kvz_oracle as orc
+from oracle import kvz_oracle_int4 as o4
+from query_agnostic_kv_kvz_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+kvz = pytest.importorskip("query_agnostic_kv_kvz_b200")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    kvz.lib()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(shape, seed, scale=1.0):
+    return (torch.randn(shape, generator=gen(seed), device="cuda") * scale).bfloat16()
+
+
+def table(rot, n_pos):
+    f, a = kvz.kvz_rotary_freqs(rot)
+    return kvz.kvz_rotary_table(f.cuda(), n_pos, a)
+
+
+def new_status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def pool(caps, d, page, seed, spare=3):
+    """Shuffled pages for heads of `caps` rows; unused bytes are 0xFF (NaN scales), unused entries -1."""
+    per = [max(1, -(-n // page)) for n in caps]
+    ids = torch.randperm(sum(per) + spare, generator=torch.Generator().manual_seed(seed))
+    pages = torch.full((len(caps), max(per)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(per):
+        pages[b, :n] = ids[at:at + n].int()
+        at += n
+    cache = torch.full((sum(per) + spare, page * d * 9 // 8), 255, dtype=torch.uint8, device="cuda")
+    return cache, pages.cuda()
+
+
+def filled(counts, d, page, seed, scale=1.0):
+    """A cache that holds random rows, written by append: (cache, pages, counts, K bits, V bits per head)."""
+    B, T = len(counts), max(1, max(counts))
+    cache, pages = pool([n + 1 for n in counts], d, page, seed)
+    k, v = rand((B, T, d), seed, scale), rand((B, T, d), seed + 1)
+    n = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    st = new_status()
+    out, _ = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros(B, dtype=torch.int32, device="cuda"), page, n_new=n,
+                                 status=st)
+    assert st.item() == 0 and torch.equal(out, n)
+    return cache, pages, n, k, v
+
+
+def offsets_of(lengths):
+    return torch.tensor([0] + list(np.cumsum(lengths)), dtype=torch.int64, device="cuda")
+
+
+def expected_bytes(cache0, pages, page, d, rows):
+    """cache0 with rows {(b, slot): (k bits, v bits)} written, by the oracle."""
+    ref = cache0.copy()
+    blocks = {}
+    for (b, slot), kv in rows.items():
+        blocks.setdefault((int(pages[b, slot // page]), slot % page // 16), []).append((slot % 16, *kv))
+    for (pid, blk), put in blocks.items():
+        view = ref[pid].reshape(page // 16, 18 * d)[blk]
+        parts = [x.copy() for x in o4.unpack_block(view, d)]
+        at = [r for r, _, _ in put]
+        for o, i in ((0, 1), (3, 2)):
+            c, s, m = o4.quantize_groups(np.stack([p[i] for p in put]))
+            parts[o][at], parts[o + 1][at], parts[o + 2][at] = c, s, m
+        view[:] = o4.pack_block(*parts)
+    return ref
+
+
+# ---------------------------------------------------------------------------
+# Writing
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,n_c,ratio,mode", [(16, 40, 0.5, "per_head"), (48, 500, 0.33, "global"),
+                                                 (64, 1000, 0.1, "global"), (1024, 3000, 0.9, "per_head"),
+                                                 (32, 1, 1.0, "per_head")])
+def test_compact_bytes(d, page, n_c, ratio, mode):
+    B = 5
+    K = rand((B, n_c, d), n_c) * torch.exp(torch.randn((B, n_c, 1), generator=gen(1), device="cuda")).bfloat16()
+    V = rand((B, n_c, d), n_c + 1)
+    K[0, 0], V[0, 0] = 0.0, 1.5                       # constant rows
+    S = synth.synthetic_scores(B, n_c, seed=n_c, device="cuda")
+    S[0, 0] = float("inf")
+    if mode == "global":
+        S[2] = 0.0                                    # a head that keeps nothing
+    idx, counts, offsets = kvz.kvz_select(S, ratio, mode)
+    cnt = counts.cpu().numpy()
+    cache, pages = pool(cnt, d, page, n_c)
+    before, st = cache.cpu().numpy(), new_status()
+    assert kvz.kvz_compact_int4(K, V, idx, counts, offsets, cache, pages, page, status=st) is cache
+    assert st.item() == 0
+    ih, oh, Kb, Vb = idx.cpu().numpy(), offsets.cpu().numpy(), bits(K), bits(V)
+    rows = {(b, p): (Kb[b, ih[oh[b] + p]], Vb[b, ih[oh[b] + p]]) for b in range(B) for p in range(cnt[b])}
+    np.testing.assert_array_equal(cache.cpu().numpy(), expected_bytes(before, pages.cpu().numpy(), page, d, rows))
+
+
+def test_compact_corner_values():
+    # NaN, infinities, a range past float32, steps under the smallest normal number, exact ties, constant groups
+    d, page = 64, 16
+    x = torch.zeros((1, 16, d))
+    x[0, 0, 3] = float("nan")
+    x[0, 1, 5], x[0, 2, 5] = float("inf"), float("-inf")
+    x[0, 3, 0], x[0, 3, 1] = 3e38, -3e38
+    x[0, 4, 7], x[0, 5, 7] = 2.0 ** -130, 2.0 ** -121
+    x[0, 6] = torch.arange(64) % 31 * 0.5             # step 1: halves are ties
+    x[0, 7] = -2.0
+    x[0, 8, :2] = torch.tensor([-0.0, 0.0])
+    x[0, 9] = torch.linspace(-1e38, 1e38, 64)
+    K = x.bfloat16().cuda()
+    V = K.flip(1).contiguous()
+    idx = torch.arange(16, dtype=torch.int32, device="cuda")
+    counts, offsets = torch.tensor([16], dtype=torch.int32, device="cuda"), offsets_of([16])
+    cache, pages = pool([16], d, page, 0)
+    before = cache.cpu().numpy()
+    kvz.kvz_compact_int4(K, V, idx, counts, offsets, cache, pages, page)
+    Kb, Vb = bits(K)[0], bits(V)[0]
+    ref = expected_bytes(before, pages.cpu().numpy(), page, d, {(0, p): (Kb[p], Vb[p]) for p in range(16)})
+    got, want = (o4.unpack_block(c[int(pages[0, 0])], d) for c in (cache.cpu().numpy(), ref))
+    for i in (0, 1, 3, 4):
+        np.testing.assert_array_equal(got[i], want[i])
+    # minima may differ in the sign of a zero: they stand for the same value
+    for i in (2, 5):
+        np.testing.assert_array_equal(orc.bf16_bits_to_f64(got[i]), orc.bf16_bits_to_f64(want[i]))
+
+
+@pytest.mark.parametrize("d,rot,il", [(128, 128, False), (128, 64, True), (64, 48, False), (64, 64, True), (64, 0, False),
+                                      (128, 96, False)])
+@pytest.mark.parametrize("T", [1, 2, 3, 37])
+def test_append_bytes(d, rot, il, T):
+    counts = [0, 1, 15, 16, 17, 30, 47, 5]
+    B, G, page = len(counts), 3, 16
+    cache, pages = pool([c + T for c in counts], d, page, T)
+    cache.copy_(torch.randint(0, 256, cache.shape, generator=gen(T), device="cuda", dtype=torch.uint8))
+    before = cache.cpu().numpy()
+    k = rand((T, B, d), T).permute(1, 0, 2)
+    v = rand((T, B, 2 * d), T + 1)[..., d:].permute(1, 0, 2)
+    q = rand((T, B, G, d), T + 2).permute(1, 2, 0, 3)
+    n_new = torch.tensor([T, T, 0, T, max(T - 1, 0), T, T // 2, T], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    pos = torch.randint(0, 900, (B, T), dtype=torch.int32, device="cuda")
+    kw = dict(positions=pos, table=table(rot, 900), interleaved=il) if rot else {}
+    q_out = torch.full((B, G, T, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    st = new_status()
+    out, qo = kvz.kvz_append_int4(k, v, cache, pages, cnt, page, q=q, q_out=q_out, n_new=n_new, status=st, **kw)
+    assert st.item() == 0 and qo is q_out
+    assert torch.equal(out, cnt + n_new)
+    kb, vb, qb = bits(k), bits(v), bits(q)
+    if rot:
+        t = kw["table"].cpu().numpy()
+        kb = o4.rotary(kb, pos.cpu().numpy(), t, il)
+        qb = o4.rotary(qb, pos.cpu().numpy()[:, None], t, il)
+    nn = n_new.cpu().numpy()
+    rows = {(b, counts[b] + i): (kb[b, i], vb[b, i]) for b in range(B) for i in range(nn[b])}
+    np.testing.assert_array_equal(cache.cpu().numpy(), expected_bytes(before, pages.cpu().numpy(), page, d, rows))
+    got = bits(q_out)
+    for b in range(B):
+        np.testing.assert_array_equal(got[b, :, :nn[b]], qb[b, :, :nn[b]])
+        assert bool((q_out[b, :, nn[b]:] == 9).all())
+
+
+def test_append_shared_positions_match_rotary():
+    # positions [T] for all heads; the appended keys are kvz_rotary's rows
+    B, T, d, page = 6, 130, 128, 32
+    t = table(d, 700)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 500
+    k, v = rand((B, T, d), 1), rand((B, T, d), 2)
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    a, pages = pool([T] * B, d, page, 1)
+    b = a.clone()
+    kvz.kvz_append_int4(k, v, a, pages, zero, page, positions=pos, table=t)
+    kvz.kvz_append_int4(kvz.kvz_rotary(k, pos, t), v, b, pages, zero, page)
+    assert torch.equal(a, b)
+
+
+def test_append_one_by_one_equals_at_once_and_compact():
+    B, T, d, page = 3, 50, 64, 16
+    k, v = rand((B, T, d), 3), rand((B, T, d), 4)
+    one, pages = pool([T] * B, d, page, 2)
+    many, whole = one.clone(), one.clone()
+    cnt = torch.zeros(B, dtype=torch.int32, device="cuda")
+    kvz.kvz_append_int4(k, v, many, pages, cnt, page)
+    nxt = torch.empty_like(cnt)
+    for i in range(T):
+        kvz.kvz_append_int4(k[:, i:i + 1], v[:, i:i + 1], one, pages, cnt, page, counts_out=nxt)
+        cnt, nxt = nxt, cnt
+    assert cnt.tolist() == [T] * B
+    idx = torch.arange(T, dtype=torch.int32, device="cuda").repeat(B)
+    kvz.kvz_compact_int4(k, v, idx, cnt, offsets_of([T] * B), whole, pages, page)
+    assert torch.equal(one, many) and torch.equal(one, whole)
+
+
+# ---------------------------------------------------------------------------
+# Reading back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("counts,page", [([1], 16), ([0, 0, 3], 16), ([100, 0, 33, 16, 15, 1, 0], 48),
+                                         ([700, 1, 2], 256)])
+def test_expand(d, counts, page):
+    cache, pages, n, k, v = filled(counts, d, page, 7)
+    gap = [c + 2 for c in counts]                     # two spare rows behind every head
+    off = offsets_of(gap)
+    K = torch.full((sum(gap), d), 3.0, dtype=torch.bfloat16, device="cuda")
+    V = K.clone()
+    st = new_status()
+    kvz.kvz_expand_int4(cache, pages, n, off, page, K_out=K, V_out=V, status=st)
+    assert st.item() == 0
+    kb, vb = bits(k), bits(v)
+    for b, c in enumerate(counts):
+        o = int(off[b])
+        for src, out in ((kb, K), (vb, V)):
+            if c:
+                ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(src[b, :c])))
+                np.testing.assert_array_equal(bits(out[o:o + c]), ref)
+            assert bool((out[o + c:o + c + 2] == 3).all())
+
+
+def test_expand_part():
+    counts = [40, 5, 17, 64, 9]
+    cache, pages, n, _, _ = filled(counts, 128, 32, 8)
+    full = kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), 32, out_rows=sum(counts))
+    first = torch.tensor([3, 5, 16, 0, 8], dtype=torch.int32, device="cuda")
+    part = [c - f for c, f in zip(counts, first.tolist())]
+    got = kvz.kvz_expand_int4(cache, pages, n, offsets_of(part), 32, first=first, out_rows=sum(part))
+    at, o = 0, 0
+    for c, f, m in zip(counts, first.tolist(), part):
+        for x, y in zip(full, got):
+            assert torch.equal(x[at + f:at + c], y[o:o + m])
+        at, o = at + c, o + m
+    none = kvz.kvz_expand_int4(cache, pages, torch.zeros_like(n), offsets_of([0] * 5), 32, out_rows=0)
+    assert none[0].shape == (0, 128)
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+def check_decode(q, cache, pages, counts, page, scale, **kw):
+    st = new_status()
+    out, lse2 = kvz.kvz_decode_int4(q, cache, pages, counts, page, scale=scale, status=st, **kw)
+    assert st.item() == 0
+    ch, ph, cn, qd = cache.cpu().numpy(), pages.cpu().numpy(), counts.cpu().numpy(), f64(q)
+    o, ls = out.cpu().double().numpy(), lse2.cpu().double().numpy()
+    for b in range(len(cn)):
+        if cn[b] == 0:
+            assert np.all(o[b] == 0) and np.all(np.isneginf(ls[b]))
+            continue
+        K, V = o4.read_head(ch, ph[b], page, q.shape[2], int(cn[b]))
+        ro, rl = orc.decode_attention(qd[b:b + 1], K.astype(np.float64), V.astype(np.float64), np.array([cn[b]]),
+                                      np.array([0, cn[b]]), scale)
+        tol, ltol = o4.decode_bound(qd[b], K, V, scale)
+        assert np.all(np.abs(o[b] - ro[0]) <= tol[:, None]), (b, np.abs(o[b] - ro[0]).max(), tol)
+        assert np.all(np.abs(ls[b] - rl[0]) <= ltol)
+    return out, lse2
+
+
+@pytest.mark.parametrize("G", [1, 3, 8])
+@pytest.mark.parametrize("counts,page,d", [
+    ([1], 16, 128),                                   # one row
+    ([15, 16, 17, 0, 31, 33, 1, 128], 16, 64),        # a block's edges, an empty head
+    ([300, 2457, 64, 5], 48, 128),                    # pages of three blocks
+    ([2457] * 8, 64, 128),                            # the pruned 8K layer
+    ([20000, 3, 0, 777], 1024, 64),
+])
+def test_decode(G, counts, page, d):
+    cache, pages, n, _, _ = filled(counts, d, page, len(counts) + G)
+    check_decode(rand((len(counts), G, d), G), cache, pages, n, page, d ** -0.5)
+
+
+def test_decode_one_long_head():
+    cache, pages, n, _, _ = filled([100003], 128, 128, 11)    # every CTA reads a part of it
+    check_decode(rand((1, 5, 128), 1), cache, pages, n, 128, 0.088)
+
+
+def test_decode_many_heads():
+    # more heads than counts kept on chip and than CTAs, many empty: every CTA's share spans several
+    counts = [(n * 7) % 40 if n % 3 else 0 for n in range(1500)]
+    cache, pages, n, _, _ = filled(counts, 64, 16, 12)
+    check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
+
+
+def test_decode_all_empty():
+    cache, pages, n, _, _ = filled([0, 0, 0], 128, 16, 13)
+    check_decode(rand((3, 4, 128), 3), cache, pages, n, 16, 0.1)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.088, 3.0])
+def test_decode_peaked_and_flat(scale):
+    # logits of hundreds in both orders: the running reference moves often, or never again
+    d, page, N = 128, 32, 600
+    k = rand((2, N, d), 14)
+    ramp = torch.linspace(0, 3, N, device="cuda").bfloat16()
+    k[0] = k[0] * ramp[:, None]
+    k[1] = k[1] * ramp.flip(0)[:, None]
+    v = rand((2, N, d), 15)
+    cache, pages = pool([N, N], d, page, 3)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    n, _ = kvz.kvz_append_int4(k, v, cache, pages, zero, page)
+    check_decode(rand((2, 8, d), 16), cache, pages, n, page, scale)
+
+
+def test_decode_ignores_rows_past_the_end():
+    # NaN scales behind the last row, in its block and on unused pages
+    counts, d, page = [1, 18, 47], 128, 16
+    cache, pages, n, k, v = filled(counts, d, page, 17)
+    bad = torch.full((3, 3, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    room = [int((pages[b] >= 0).sum()) * page - c for b, c in enumerate(counts)]
+    n_bad = torch.tensor([min(3, r) for r in room], dtype=torch.int32, device="cuda")
+    kvz.kvz_append_int4(bad, bad, cache, pages, n, page, n_new=n_bad)
+    out, _ = check_decode(rand((3, 4, d), 18), cache, pages, n, page, 0.1)
+    assert bool(torch.isfinite(out).all())
+    # a NaN row that does count reaches its head's output and no other's
+    n2 = n.clone()
+    n2[1] += 1
+    out2, _ = kvz.kvz_decode_int4(rand((3, 4, d), 18), cache, pages, n2, page, scale=0.1)
+    assert bool(torch.isnan(out2[1]).all()) and torch.equal(out2[0], out[0]) and torch.equal(out2[2], out[2])
+
+
+def test_decode_matches_decode_over_expanded_rows():
+    counts, d, page = [500, 33, 2000, 0], 128, 64
+    cache, pages, n, _, _ = filled(counts, d, page, 19)
+    q = rand((4, 4, d), 20)
+    out, lse2 = kvz.kvz_decode_int4(q, cache, pages, n, page)
+    K, V = kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), page, out_rows=sum(counts))
+    o2, l2 = kvz.kvz_decode(q, K, V, n, offsets_of(counts), 2000)
+    # the expanded rows carry a bf16 rounding, 2^-8 of a value: a logit moves by 2^-8 sum |q k| scale at most
+    dl = 2.0 ** -8 * (q.float().abs().sum(-1).max().item() * K.float().abs().max().item()) * d ** -0.5
+    tol = (2 * dl + 2.0 ** -8) * V.float().abs().max().item() + 1e-4
+    assert (out - o2).abs().max().item() <= tol
+    assert torch.equal(torch.isneginf(lse2), torch.isneginf(l2))
+
+
+def test_decode_shared_pages():
+    # two heads that name the same pages read the same rows
+    cache, pages, n, _, _ = filled([200, 200], 64, 16, 21)
+    pages[1] = pages[0]
+    q = rand((1, 4, 64), 22).expand(2, 4, 64).contiguous()
+    out, lse2 = check_decode(q, cache, pages, n, 16, 0.125)
+    assert torch.allclose(out[0], out[1], atol=1e-5)
+
+
+def test_decode_is_deterministic_and_leaves_inputs():
+    cache, pages, n, _, _ = filled([5000, 40, 9000, 123], 128, 64, 23)
+    q, c0 = rand((4, 8, 128), 24), cache.clone()
+    ws = torch.full((kvz.kvz_decode_int4_workspace_size(8, 128),), 255, dtype=torch.uint8, device="cuda")
+    a = kvz.kvz_decode_int4(q, cache, pages, n, 64, workspace=ws)
+    for _ in range(3):
+        b = kvz.kvz_decode_int4(q, cache, pages, n, 64, workspace=ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(cache, c0)
+
+
+def test_offsets_past_32_bits():
+    # pages that lie 2^32 bytes and more into the pool
+    d, page = 128, 64
+    cache = torch.empty((600000, page * 144), dtype=torch.uint8, device="cuda")
+    pages = torch.tensor([[599999, 470000], [3, 466034]], dtype=torch.int32, device="cuda")
+    k, v = rand((2, 100, d), 25), rand((2, 100, d), 26)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    n, _ = kvz.kvz_append_int4(k, v, cache, pages, zero, page)
+    K, V = kvz.kvz_expand_int4(cache, pages, n, offsets_of([100, 100]), page, out_rows=200)
+    for src, got in ((k, K), (v, V)):
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(src).reshape(200, d))))
+        np.testing.assert_array_equal(bits(got), ref)
+    small = cache[pages.flatten().long()].clone()
+    q = rand((2, 4, d), 27)
+    a = kvz.kvz_decode_int4(q, cache, pages, n, page)
+    b = kvz.kvz_decode_int4(q, small, torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda"), n, page)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ---------------------------------------------------------------------------
+# Device-detected errors
+# ---------------------------------------------------------------------------
+def test_bad_counts_are_left_out():
+    counts, d, page = [100, 50, 60], 128, 16
+    cache, pages, n, _, _ = filled(counts, d, page, 28)
+    q = rand((3, 2, d), 29)
+    good = kvz.kvz_decode_int4(q, cache, pages, n, page)
+    for bad in (-1, pages.shape[1] * page + 1):
+        m = n.clone()
+        m[1] = bad
+        st = new_status()
+        out = torch.full((3, 2, d), 5.0, device="cuda")
+        kvz.kvz_decode_int4(q, cache, pages, m, page, out=out, status=st)
+        assert st.item() == 1 and bool((out[1] == 5).all())
+        assert torch.allclose(out[0], good[0][0], atol=1e-5) and torch.allclose(out[2], good[0][2], atol=1e-5)
+        K = torch.full((210, d), 5.0, dtype=torch.bfloat16, device="cuda")
+        st = new_status()
+        kvz.kvz_expand_int4(cache, pages, m, offsets_of(counts), page, K_out=K, V_out=K.clone(), status=st)
+        assert st.item() == 1 and bool((K[100:150] == 5).all()) and not bool((K[:100] == 5).all())
+        st, c0 = new_status(), cache.clone()
+        k = rand((3, 1, d), 30)
+        out_n, _ = kvz.kvz_append_int4(k, k, cache, pages, m, page, status=st)
+        assert st.item() == 1 and out_n[1].item() == bad
+        p1 = pages[1][pages[1] >= 0].long()
+        assert torch.equal(cache[p1], c0[p1])
+        cache.copy_(c0)
+
+
+def test_bad_pages_are_reported():
+    counts, d, page = [40, 40], 64, 16
+    cache, pages, n, _, _ = filled(counts, d, page, 31)
+    k = rand((2, 1, d), 32)
+    for bad in (-1, cache.shape[0], 2 ** 31 - 1):
+        p = pages.clone()
+        p[1, 2] = bad
+        st, c0 = new_status(), cache.clone()
+        out_n, _ = kvz.kvz_append_int4(k, k, cache, p, n, page, status=st)
+        assert st.item() == 1 and out_n.tolist() == [41, 40]
+        p0 = pages[0][pages[0] >= 0].long()
+        c0[p0] = cache[p0]
+        assert torch.equal(cache, c0)
+        st = new_status()
+        out, _ = kvz.kvz_decode_int4(rand((2, 2, d), 33), cache, p, n, page, status=st)
+        assert st.item() == 1 and bool(torch.isfinite(out[0]).all())
+        st = new_status()
+        K = torch.full((80, d), 5.0, dtype=torch.bfloat16, device="cuda")
+        kvz.kvz_expand_int4(cache, p, n, offsets_of(counts), page, K_out=K, V_out=K.clone(), status=st)
+        assert st.item() == 1 and bool((K[72:] == 5).all()) and not bool((K[40:72] == 5).any())
+
+
+def test_append_refusals_on_the_device():
+    d, page = 64, 16
+    cache, pages, n, _, _ = filled([30, 30, 30, 30], d, page, 34)
+    cap = pages.shape[1] * page
+    c0 = cache.clone()
+    k = rand((4, 3, d), 35)
+    t = table(64, 20)
+    pos = torch.tensor([[1, 2, 3], [4, 25, 5], [0, 1, 2], [3, 3, 3]], dtype=torch.int32, device="cuda")
+    n_new = torch.tensor([4, 2, -1, 1], dtype=torch.int32, device="cuda")
+    st = new_status()
+    out_n, _ = kvz.kvz_append_int4(k, k, cache, pages, n, page, positions=pos, table=t, n_new=n_new, status=st)
+    assert st.item() == 1 and out_n.tolist() == [30, 30, 30, 31] and cap == 32
+    for b in (0, 2):
+        ids = pages[b].long()
+        assert torch.equal(cache[ids], c0[ids])
+    # a run that would pass the table's last page
+    st, c1 = new_status(), cache.clone()
+    out_n, _ = kvz.kvz_append_int4(k, k, cache, pages, n, page, status=st)
+    assert st.item() == 1 and out_n.tolist() == [30] * 4 and torch.equal(cache, c1)
+
+
+def test_compact_reports_bad_idx_and_counts():
+    B, n_c, d, page = 2, 100, 64, 16
+    K, V = rand((B, n_c, d), 36), rand((B, n_c, d), 37)
+    idx = torch.arange(20, dtype=torch.int32, device="cuda").repeat(2)
+    idx[3], idx[25] = n_c, -1
+    counts = torch.tensor([20, 20], dtype=torch.int32, device="cuda")
+    cache, pages = pool([20, 20], d, page, 4)
+    st = new_status()
+    kvz.kvz_compact_int4(K, V, idx, counts, offsets_of([20, 20]), cache, pages, page, status=st)
+    assert st.item() == 1
+    Kx, _ = kvz.kvz_expand_int4(cache, pages, counts, offsets_of([20, 20]), page, out_rows=40)
+    assert bool((Kx[3] == 0).all()) and bool((Kx[25] == 0).all()) and not bool((Kx[4] == 0).all())
+    st, c0 = new_status(), cache.clone()
+    idx[3], idx[25] = 3, 5
+    counts[1] = 21                                    # more than its run of idx
+    kvz.kvz_compact_int4(V, K, idx, counts, offsets_of([20, 20]), cache, pages, page, status=st)
+    assert st.item() == 1
+    p1 = pages[1].long()
+    assert torch.equal(cache[p1], c0[p1]) and not torch.equal(cache[pages[0].long()], c0[pages[0].long()])
+
+
+# ---------------------------------------------------------------------------
+# Streams, graphs, and the whole path
+# ---------------------------------------------------------------------------
+def test_streams():
+    cache, pages, n, _, _ = filled([900, 4000], 128, 64, 38)
+    q = rand((2, 4, 128), 39)
+    ref = kvz.kvz_decode_int4(q, cache, pages, n, 64)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for i in range(6):                                # two streams at once, scratch allocated by each call
+        s = sides[i % 2]
+        s.wait_stream(torch.cuda.current_stream())
+        outs.append(kvz.kvz_decode_int4(q, cache, pages, n, 64, stream=s if i < 4 else s.cuda_stream))
+    for s in sides:
+        s.synchronize()
+    for o, l2 in outs:
+        assert torch.equal(o, ref[0]) and torch.equal(l2, ref[1])
+
+
+def test_decoding_in_graphs_that_share_a_workspace():
+    # one graph appends, another attends, a third attends over another cache with the same workspace; replayed in turn
+    d, page, B, G = 128, 16, 3, 4
+    counts = [100, 7, 250]
+    cache, pages = pool([c + 8 for c in counts], d, page, 5)
+    k0, v0 = rand((B, 250, d), 40), rand((B, 250, d), 41)
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    n0 = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    kvz.kvz_append_int4(k0, v0, cache, pages, zero, page, n_new=n0)
+    other = filled([33, 500, 1], d, page, 42)
+    ws = torch.empty(kvz.kvz_decode_int4_workspace_size(G, d), dtype=torch.uint8, device="cuda")
+    cnt, nxt = n0.clone(), n0.clone()
+    k, v, q = rand((B, 1, d), 43), rand((B, 1, d), 44), rand((B, G, 1, d), 45)
+    t = table(d, 400)
+    pos = n0[:, None].clone()
+    q_out = torch.empty_like(q)
+    out, lse2 = torch.empty((B, G, d), device="cuda"), torch.empty((B, G), device="cuda")
+    out2 = torch.empty((B, G, d), device="cuda")
+    g1, g2, g3 = (torch.cuda.CUDAGraph() for _ in range(3))
+    with torch.cuda.graph(g1):
+        kvz.kvz_append_int4(k, v, cache, pages, cnt, page, positions=pos, table=t, q=q, q_out=q_out, counts_out=nxt)
+        cnt.copy_(nxt)
+        pos.add_(1)
+    with torch.cuda.graph(g2):
+        kvz.kvz_decode_int4(q_out.view(B, G, d), cache, pages, cnt, page, out=out, lse2=lse2, workspace=ws)
+    with torch.cuda.graph(g3):
+        kvz.kvz_decode_int4(q_out.view(B, G, d), other[0], other[1], other[2], page, out=out2, lse2=lse2, workspace=ws)
+    for step in range(5):
+        for x, s in ((k, 50), (v, 60), (q, 70)):
+            x.copy_(rand(tuple(x.shape), s + step))
+        g1.replay()
+        g2.replay()
+        got = out.clone()
+        g3.replay()
+        torch.cuda.synchronize()
+        assert cnt.tolist() == [c + step + 1 for c in counts]
+        ref, _ = check_decode(q_out.view(B, G, d), cache, pages, cnt, page, d ** -0.5)
+        assert torch.equal(got, ref)
+        assert torch.equal(out2, kvz.kvz_decode_int4(q_out.view(B, G, d), other[0], other[1], other[2], page)[0])
+
+
+def test_whole_path_from_scores_to_answers():
+    # score, select, compact into four bits, then tokens one by one: the cache equals the oracle's, byte for byte,
+    # and so does what every step attends to
+    w = synth.WORKLOADS["tiny"]
+    x = synth.layer_inputs(w, device="cuda:0")
+    B, G, d, page, steps = w.B, w.G, w.d, 16, 6
+    t = table(d, 400)
+    pos_ctx = torch.arange(w.n_c[0], dtype=torch.int32, device="cuda")
+    pos_in = torch.arange(w.n_in(), dtype=torch.int32, device="cuda") + w.n_c[0]
+    t_in = table(d, int(pos_in[-1]) + 1)
+    K_ctx = kvz.kvz_rotary(x["K_ctx"], pos_ctx, t_in)
+    S = kvz.kvz_score(kvz.kvz_rotary(x["Q"], pos_in, t_in), K_ctx, kvz.kvz_rotary(x["K_in"], pos_in, t_in))
+    idx, counts, offsets = kvz.kvz_select(S, w.ratio, w.mode)
+    kept = int(offsets[-1])
+    cache, pages = pool([kept + steps], d, page, 6)
+    before, st = cache.cpu().numpy(), new_status()
+    kvz.kvz_compact_int4(K_ctx, x["V"], idx, counts, offsets, cache, pages, page, status=st)
+    ih, Kb, Vb = idx.cpu().numpy(), bits(K_ctx)[0], bits(x["V"])[0]
+    rows = {(0, p): (Kb[ih[p]], Vb[ih[p]]) for p in range(kept)}
+    n = counts
+    for i in range(steps):
+        k, v, q = rand((1, 1, d), 80 + i), rand((1, 1, d), 90 + i), rand((1, G, 1, d), 100 + i)
+        pos = torch.tensor([w.n_c[0] + i], dtype=torch.int32, device="cuda")   # positions go on from the whole context
+        n, qr = kvz.kvz_append_int4(k, v, cache, pages, n, page, positions=pos, table=t, q=q, status=st)
+        rows[(0, kept + i)] = (o4.rotary(bits(k), pos.cpu().numpy(), t.cpu().numpy())[0, 0], bits(v)[0, 0])
+        check_decode(qr.view(1, G, d), cache, pages, n, page, d ** -0.5)
+    assert st.item() == 0 and n.tolist() == [kept + steps]
+    np.testing.assert_array_equal(cache.cpu().numpy(), expected_bytes(before, pages.cpu().numpy(), page, d, rows))
