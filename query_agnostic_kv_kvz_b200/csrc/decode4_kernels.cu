@@ -3,15 +3,23 @@
 //   out[b, g] = sum_j softmax_j(scale * <q_g, k_j>) v_j,
 //   k_j = s_j code_j + m_j (and v_j alike) per group of 64 dims.
 //
-// The codes are whole numbers, exact in bf16, so both products run on them
+// The codes are whole numbers, exact in fp16, so both products run on them
+// (mma.sync m16n8k16: the G <= 8 queries are below the 64 rows of tcgen05,
+// whose operands would have to be widened into shared or tensor memory first)
 // and the scales are applied to what comes out:
-//   <q, k_j> = sum_groups s_j <q, code_j> + m_j sum(q)
-//   out = sum_groups sum_j (p_j s_j) code_j + p_j m_j
-// A code is widened to bf16 as 16 + code (its four bits are mantissa bits 3
-// to 6 of a number in [16, 32)): one shift and one three-input logic
-// instruction per two codes.  The 16s leave with sum(q) and sum(p s), in
-// float32.  p s is split exactly into three bf16 parts (8 + 8 + 8 bits of
-// its 24), so the result keeps float32 accuracy.
+//   <q, k_j> = sum_groups s_j <q, code_j - 8> + (m_j + 8 s_j) sum(q)
+//   out = sum_groups sum_j (p_j s_j) (code_j - 8) + p_j (m_j + 8 s_j)
+// Two codes of a word widen with one logic instruction, to 1024 + 2^i code
+// (code bits as low mantissa bits), and one fp16 multiply-add, to code - 8.
+// Taking 8 off matters: a sum over many rows of values around 0 is far
+// smaller than the same sum of 0..15, and would drown in the latter's
+// rounding.  The tensor core truncates what it adds to, so it sums 32 rows at
+// a time and the running output adds those in float32.
+//
+// fp16 operands: q is scaled by a power of two to a largest entry of 2^14
+// (bf16's 8 bits stay exact down to 2^-38 of it); a weight p s, scaled by a
+// power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
+// for s), is the sum of two fp16 numbers, 22 bits.
 //
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At that
 // rate an SM has to widen and multiply a row (both of K and V, all queries)
@@ -19,8 +27,8 @@
 //
 // One CTA of 8 warps takes an equal share of the blocks of all heads, whatever
 // the heads' lengths (a share may end one head and begin others).  A warp
-// brings its blocks in by bulk copy through a ring of its own, one copy per
-// 16-row block, and keeps a running (reference, sum, output) per query; the
+// brings its blocks in by bulk copy through a ring of its own, 32 rows a stage
+// (one copy where they share a page), and keeps a running (reference, sum, output) per query; the
 // warps merge in shared memory at the end of each head's part.  A head that
 // several CTAs read leaves one partial per CTA, which a second launch joins
 // in order: no atomics, and identical inputs give identical results.
@@ -39,16 +47,17 @@ namespace {
 
 constexpr int kD4Warps = 8;
 constexpr int kD4Threads = kD4Warps * 32;
-constexpr int kD4Stages = 4;
-constexpr int kD4MinBlocks = kD4Warps;                        // a CTA's share is at least a block per warp
+constexpr int kD4Stages = 2;
+constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share is at least a stage per warp
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
-constexpr float kD4Slack = 8.0f;                              // log2 by which a logit may pass the reference
+constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
 
 template <int D>
 struct D4 {
   static constexpr int KS = D / 16;                           // k-steps of Q K^T
   static constexpr int MT = D / 16;                           // 16-dim tiles of the output
-  static constexpr int RING = kD4Warps * kD4Stages * C4<D>::BLOCK;
+  static constexpr int STAGE = 2 * C4<D>::BLOCK;              // 32 rows
+  static constexpr int RING = kD4Warps * kD4Stages * STAGE;
   static constexpr int O_OFF = RING;                          // float [warps][8][D]
   static constexpr int SMEM = RING + kD4Warps * 8 * D * 4;
 };
@@ -57,7 +66,7 @@ static_assert(D4<128>::SMEM <= 107 * 1024, "two CTAs per SM");
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
@@ -67,8 +76,41 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two codes of a word, in bits 3..6 of its halves after the shift, as bf16 16 + code.
-__device__ __forceinline__ uint32_t wide2(uint32_t w) { return (w & 0x00780078u) | 0x41804180u; }
+__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Two codes, one in each half of w, as fp16 code - 8 (exact): 1024 + code * 2^SH is
+// scaled by 2^-SH and brought down.  SH is where the codes' four bits start.
+template <int SH>
+__device__ __forceinline__ uint32_t wide2(uint32_t w) {
+  static_assert(SH == 0 || SH == 3 || SH == 4, "");
+  constexpr uint32_t mask = 0x000F000Fu << SH;
+  constexpr uint32_t mul = SH == 0 ? 0x3C003C00u : (SH == 3 ? 0x30003000u : 0x2C002C00u);      // 1, 1/8, 1/16
+  constexpr uint32_t add = SH == 0 ? 0xE408E408u : (SH == 3 ? 0xD840D840u : 0xD480D480u);      // -1032, -136, -72
+  return fma_h2((w & mask) | 0x64006400u, mul, add);
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float h_lo(uint32_t w) {
+  float f;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(f) : "r"(w));
+  return f;
+}
+__device__ __forceinline__ float h_hi(uint32_t w) {
+  float f;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h;}" : "=f"(f) : "r"(w));
+  return f;
+}
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 template <int N>
 __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -177,9 +219,9 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   int64_t b = s_find[0], start = s_find[1];
 
   uint64_t* bar = full + warp * kD4Stages;
-  uint8_t* ring = smem + warp * (kD4Stages * L::BLOCK);
+  uint8_t* ring = smem + warp * (kD4Stages * S::STAGE);
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
-  uint32_t used = 0;                                          // blocks this warp has taken from its ring
+  uint32_t used = 0;                                          // stages this warp has taken from its ring
   int4 cont = make_int4(-1, 0, 0, 0);
 
   for (;;) {
@@ -187,197 +229,267 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     const int64_t n_blk = blocks_of(count, p.cap);
     const int a0 = static_cast<int>(u0 > start ? u0 - start : 0);
     const int a1 = static_cast<int>(u1 - start < n_blk ? u1 - start : n_blk);
-    const int n = a1 - a0 > warp ? (a1 - a0 - warp + kD4Warps - 1) / kD4Warps : 0;   // this warp's blocks
+    const int n_st = (a1 - a0 + 1) / 2;                       // 32-row stages of this part; warp w takes w, w + 8, ...
+    const int n = n_st > warp ? (n_st - warp + kD4Warps - 1) / kD4Warps : 0;
+    auto blk_of = [&](int i) -> int { return a0 + 2 * (warp + kD4Warps * i); };
 
-    // lane 0 keeps the ring full: block i of the warp is block a0 + warp + 8 i of the head
+    // lane 0 keeps the ring full
     const int32_t* const row_pages = p.pg.pages + b * p.pg.max_pages;
-    auto page_id = [&](int i) -> int {
-      return i < n ? __ldg(row_pages + page_of(p.pg, static_cast<uint32_t>(a0 + warp + kD4Warps * i))) : 0;
+    auto page_ids = [&](int i) -> int2 {
+      if (i >= n) return make_int2(0, 0);
+      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
+      const uint32_t p0 = page_of(p.pg, blk);
+      const uint32_t p1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : p0;
+      return make_int2(__ldg(row_pages + p0), __ldg(row_pages + p1));
     };
-    auto issue = [&](int i, uint32_t ahead, int id) {          // `ahead`: how far past the block now taken
-      const uint32_t blk = static_cast<uint32_t>(a0 + warp + kD4Warps * i);
-      if (id < 0 || id >= p.pg.n_pages) {                     // reported; page 0 stands in, so the read stays inside
-        report(p.status, KVZ_ERR_INVALID_ARG);
-        id = 0;
-      }
+    auto valid_id = [&](int id) -> int64_t {                  // page 0 stands in, so the read stays inside
+      if (id >= 0 && id < p.pg.n_pages) return id;
+      report(p.status, KVZ_ERR_INVALID_ARG);
+      return 0;
+    };
+    auto issue = [&](int i, uint32_t ahead, int2 id) {        // `ahead`: how far past the stage now taken
+      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
+      const uint32_t p0 = page_of(p.pg, blk), in0 = blk - p0 * p.pg.blocks;
       const uint32_t st = (used + ahead) % kD4Stages;
-      mbar_arrive_expect_tx(&bar[st], L::BLOCK);
-      bulk_load(ring + st * L::BLOCK,
-                p.pg.cache + (static_cast<int64_t>(id) * p.pg.blocks + (blk - page_of(p.pg, blk) * p.pg.blocks)) *
-                                 L::BLOCK,
-                L::BLOCK, &bar[st]);
+      uint8_t* dst = ring + st * S::STAGE;
+      const uint8_t* src0 = p.pg.cache + (valid_id(id.x) * p.pg.blocks + in0) * L::BLOCK;
+      const bool two = static_cast<int>(blk) + 1 < a1;
+      mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
+      if (two && in0 + 1 < p.pg.blocks) {
+        bulk_load(dst, src0, 2 * L::BLOCK, &bar[st]);
+      } else {
+        bulk_load(dst, src0, L::BLOCK, &bar[st]);
+        if (two) bulk_load(dst + L::BLOCK, p.pg.cache + valid_id(id.y) * p.pg.blocks * L::BLOCK, L::BLOCK, &bar[st]);
+      }
     };
     __syncthreads();                                          // barriers are initialised; s_o of the last part is read
-    int id_next = 0;
+    int2 id_next = make_int2(0, 0);
     if (lane == 0) {
-      int id[kD4Stages];
+      int2 id[kD4Stages];
 #pragma unroll
-      for (int i = 0; i < kD4Stages; ++i) id[i] = page_id(i);
-      id_next = page_id(kD4Stages);
+      for (int i = 0; i < kD4Stages; ++i) id[i] = page_ids(i);
+      id_next = page_ids(kD4Stages);
 #pragma unroll
       for (int i = 0; i < kD4Stages; ++i)
         if (i < n) issue(i, i, id[i]);
     }
 
-    // Q fragments (rows = queries; rows >= G are zero) and -16 sum(q), sum(q) per group
+    // Q fragments (rows = queries; rows >= G are zero), scaled by a power of two
+    // to a largest exponent of 14, and sum(q) per group
     uint32_t qa[S::KS][2];
-    float qs[NG];
+    float qs[NG], c2;
+    {
+      uint4 v[NG][2];
+      uint32_t ef = 0;                                        // largest exponent field of the row
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      float sum = 0.0f;
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < G) v = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
-        qa[4 * g + 2 * u][0] = v.x, qa[4 * g + 2 * u][1] = v.y;
-        qa[4 * g + 2 * u + 1][0] = v.z, qa[4 * g + 2 * u + 1][1] = v.w;
-        sum += ((bf_lo(v.x) + bf_hi(v.x)) + (bf_lo(v.y) + bf_hi(v.y))) +
-               ((bf_lo(v.z) + bf_hi(v.z)) + (bf_lo(v.w) + bf_hi(v.w)));
+        for (int u = 0; u < 2; ++u) {
+          v[g][u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
+          const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
+        }
+      ef = max(ef, __shfl_xor_sync(kFullMask, ef, 1));
+      ef = max(ef, __shfl_xor_sync(kFullMask, ef, 2));
+      // an infinity or NaN stays one whatever the factor; an exponent below -112 needs no more than 2^126
+      const uint32_t fe = ef == 255u || ef == 0u ? 127u : min(268u - ef, 253u);
+      const float f = __uint_as_float(fe << 23);
+      c2 = p.c2 * __uint_as_float((254u - fe) << 23);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = bf_lo(w[k]) * f, x1 = bf_hi(w[k]) * f;
+            qa[4 * g + 2 * u + k / 2][k % 2] = pack_h2(x0, x1);
+            sum += x0 + x1;
+          }
+        }
+        sum += __shfl_xor_sync(kFullMask, sum, 1);
+        sum += __shfl_xor_sync(kFullMask, sum, 2);
+        qs[g] = sum;
       }
-      sum += __shfl_xor_sync(kFullMask, sum, 1);
-      sum += __shfl_xor_sync(kFullMask, sum, 2);
-      qs[g] = sum;
     }
 
-    float o[S::MT][4];                                        // out^T tiles: dims x queries 2c, 2c + 1
+    float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
 #pragma unroll
     for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
     float m_ref = -INFINITY, thr = -INFINITY;                 // of query r
     float l_run = 0.0f;                                       // of query r, this lane's keys
-    float om[NG];                                             // sum of p (m - 16 s), the same
+    float om[NG];                                             // sum of p (m + 8 s), the same
 #pragma unroll
     for (int g = 0; g < NG; ++g) om[g] = 0.0f;
+    float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
 
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const uint32_t st = used % kD4Stages;
       ok = mbar_wait_warp(&bar[st], (used / kD4Stages) & 1u, abort_flag, p.status);
       if (!ok) break;                                         // warp-uniform
-      const uint8_t* blk = ring + st * L::BLOCK;
+      const uint8_t* stage = ring + st * S::STAGE;
+      const int blk0 = blk_of(i);
+      // rows of the stage that count: the head may end inside it, and this CTA's share after its first block (what
+      // lies past them, in the page or left in the stage, has no influence)
+      const int rows = min(count - blk0 * kC4Rows, (a1 - blk0) * kC4Rows);
 
-      // ---- scores of query r and keys 8t + 2c + e of the block
-      float x[2][2];
+      // ---- scores of query r and keys 16k + 8t + 2c + e of the stage
+      float x[2][2][2];
+      uint32_t vp[2][2][2 * NG];                              // V scales of the same keys
+      uint32_t vmax = 0u;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        uint32_t kw[2 * NG], kp[2 * NG];
-        lds_words(blk + (8 * t + r) * (D / 2) + c * (8 * NG), kw);
-        lds_words(blk + L::KS_OFF + (8 * t + 2 * c) * (4 * NG), kp);
-        x[t][0] = x[t][1] = 0.0f;
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc[4];
-          const float init = -16.0f * qs[g];
+        for (int t = 0; t < 2; ++t) {
+          const uint8_t* blk = stage + k * L::BLOCK;
+          uint32_t kw[2 * NG], kp[2 * NG];
+          lds_words(blk + (8 * t + r) * (D / 2) + c * (8 * NG), kw);
+          lds_words(blk + L::KS_OFF + (8 * t + 2 * c) * (4 * NG), kp);
+          lds_words(blk + L::VS_OFF + (8 * t + 2 * c) * (4 * NG), vp[k][t]);
+          x[k][t][0] = x[k][t][1] = 0.0f;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t w = kw[2 * g + u];
-            const uint32_t(&q0)[2] = qa[4 * g + 2 * u], (&q1)[2] = qa[4 * g + 2 * u + 1];
-            if (u == 0)
-              mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2(w), wide2(w >> 4), init, init, 0.0f, 0.0f);
-            else
-              mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2(w), wide2(w >> 4), acc[0], acc[1], acc[2], acc[3]);
-            mma_16816(acc, q1[0], 0u, q1[1], 0u, wide2(w >> 8), wide2(__funnelshift_r(w, w, 12)), acc[0], acc[1],
-                      acc[2], acc[3]);
-          }
+          for (int g = 0; g < NG; ++g) {
+            float acc[4];
+            const float init = 8.0f * qs[g];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t sm = kp[e * NG + g];
-            x[t][e] = fmaf(bf_lo(sm), acc[e], fmaf(bf_hi(sm), qs[g], x[t][e]));
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t w = kw[2 * g + u], w7 = w >> 7;
+              const uint32_t(&q0)[2] = qa[4 * g + 2 * u], (&q1)[2] = qa[4 * g + 2 * u + 1];
+              if (u == 0)
+                mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2<3>(w), wide2<0>(w7), init, init, 0.0f, 0.0f);
+              else
+                mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2<3>(w), wide2<0>(w7), acc[0], acc[1], acc[2], acc[3]);
+              mma_16816(acc, q1[0], 0u, q1[1], 0u, wide2<4>(w7), wide2<3>(__funnelshift_r(w, w, 12)), acc[0], acc[1],
+                        acc[2], acc[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t sm = kp[e * NG + g];
+              x[k][t][e] = fmaf(bf_lo(sm), acc[e], fmaf(bf_hi(sm), qs[g], x[k][t][e]));
+            }
           }
         }
-      }
-      uint32_t vp[2][2 * NG];                                 // V scales of the same keys
+      if (rows < 2 * kC4Rows) {                               // warp-uniform
 #pragma unroll
-      for (int t = 0; t < 2; ++t) lds_words(blk + L::VS_OFF + (8 * t + 2 * c) * (4 * NG), vp[t]);
-      const int rows = count - (a0 + warp + kD4Warps * i) * kC4Rows;
-      if (rows < kC4Rows) {                                   // the head's last block: rows past its end do not count,
-#pragma unroll                                                // whatever the page holds there
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (16 * k + 8 * t + 2 * c + e >= rows) {
+                x[k][t][e] = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) vp[k][t][e * NG + g] = 0u;
+              }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (8 * t + 2 * c + e >= rows) {
-              x[t][e] = -INFINITY;
+          for (int w = 0; w < 2 * NG; ++w) vmax = max_bf2(vmax, vp[k][t][w]);
+      // ---- softmax against a reference that moves only when a logit passes it by 2^7; the steps' scale likewise
+      float xm = -INFINITY;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) vp[t][e * NG + g] = 0u;
-            }
-      }
-      // ---- softmax against a reference that moves only when a logit passes it by 2^8
-      const float xm = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-      if (__any_sync(kFullMask, xm > thr)) {
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) xm = fmaxf(xm, fmaxf(x[k][t][0], x[k][t][1]));
+      if (__any_sync(kFullMask, xm > thr || bf_lo(vmax) > s_top)) {
         float mx = fmaxf(xm, __shfl_xor_sync(kFullMask, xm, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
         const bool up = mx > thr;
-        const float mn = up ? mx * p.c2 : m_ref;
+        const float mn = up ? mx * c2 : m_ref;
         const float alpha = up ? ex2(m_ref - mn) : 1.0f;      // 0 the first time
         if (up) {
           m_ref = mn;
-          thr = (mn + kD4Slack) / p.c2;
+          thr = (mn + kD4Slack) / c2;
           l_run *= alpha;
 #pragma unroll
           for (int g = 0; g < NG; ++g) om[g] *= alpha;
         }
-        const float al0 = __shfl_sync(kFullMask, alpha, 8 * c), al1 = __shfl_sync(kFullMask, alpha, 8 * c + 4);
+        // the power of two past the largest step (at least 2^-100, at most 2^126), twice that for room
+        const uint32_t top = __reduce_max_sync(kFullMask, __float_as_uint(bf_lo(vmax)));
+        float beta = 1.0f;
+        if (__uint_as_float(top) > s_top) {
+          const uint32_t e2 = min(max((top >> 23) + 2u, 27u), 253u);
+          const float s_new = __uint_as_float(e2 << 23);
+          beta = s_top / s_new;                               // 0 the first time
+          s_top = s_new;
+          s_mul = __uint_as_float((254u + 7u - e2) << 23);
+        }
+        const float al0 = __shfl_sync(kFullMask, alpha, 8 * c) * beta;
+        const float al1 = __shfl_sync(kFullMask, alpha, 8 * c + 4) * beta;
 #pragma unroll
         for (int t = 0; t < S::MT; ++t) {
           o[t][0] *= al0, o[t][1] *= al1;
           o[t][2] *= al0, o[t][3] *= al1;
         }
       }
-      float pr[2][2];
+      float pr[2][2][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          pr[t][e] = ex2(fmaf(x[t][e], p.c2, -m_ref));
-          l_run += pr[t][e];
-        }
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            pr[k][t][e] = ex2(fmaf(x[k][t][e], c2, -m_ref));
+            l_run += pr[k][t][e];
+          }
 
       // ---- out^T += V^T (p s)
-      uint32_t vw[2][2 * NG];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) lds_words(blk + L::V_OFF + (4 * t + c) * D + r * (8 * NG), vw[t]);
+      for (int g = 0; g < NG; ++g) {
+        uint32_t vw[2][2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            lds_words(stage + k * L::BLOCK + L::V_OFF + (4 * t + c) * D + (r * NG + g) * 8, vw[k][t]);
+        uint32_t hi[2][2], lo[2][2];                          // the weights p s 2^(7 - E) = hi + lo
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float s0 = bf_lo(vp[k][t][g]), s1 = bf_lo(vp[k][t][NG + g]);
+            const float p0 = pr[k][t][0], p1 = pr[k][t][1];
+            om[g] = fmaf(p0, fmaf(8.0f, s0, bf_hi(vp[k][t][g])), om[g]);
+            om[g] = fmaf(p1, fmaf(8.0f, s1, bf_hi(vp[k][t][NG + g])), om[g]);
+            const float w0 = p0 * (s0 * s_mul), w1 = p1 * (s1 * s_mul);
+            hi[k][t] = pack_h2(w0, w1);
+            lo[k][t] = pack_h2(w0 - h_lo(hi[k][t]), w1 - h_hi(hi[k][t]));
+          }
+#pragma unroll
+        for (int wl = 0; wl < 2; ++wl)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {                       // dims 64g + 8r + 4wl + 2h, + 1
+            uint32_t a[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t y0 = vw[k][0][wl], y1 = vw[k][1][wl];
+              if (h == 1) y0 >>= 8, y1 >>= 8;
+              a[k][0] = wide2<0>(y0), a[k][1] = wide2<4>(y0), a[k][2] = wide2<0>(y1), a[k][3] = wide2<4>(y1);
+            }
+            float d[4];
+            mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+            mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1], d[0], d[1], d[2], d[3]);
+            mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], hi[0][0], hi[0][1], d[0], d[1], d[2], d[3]);
+            mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], hi[1][0], hi[1][1], d[0], d[1], d[2], d[3]);
+            float(&acc)[4] = o[4 * g + 2 * wl + h];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += d[j];
+          }
+      }
       __syncwarp();
-      if (lane == 0 && i + kD4Stages < n) {                   // the stage is in registers: refill it
-        const int id = id_next;
-        id_next = page_id(i + kD4Stages + 1);
+      if (lane == 0 && i + kD4Stages < n) {                   // the stage is read: refill it
+        const int2 id = id_next;
+        id_next = page_ids(i + kD4Stages + 1);
         issue(i + kD4Stages, kD4Stages, id);
       }
       ++used;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint32_t part[3][2];                                  // [hi, mid, lo][t]
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float w0, w1;
-          {
-            const float s0 = bf_lo(vp[t][g]), s1 = bf_lo(vp[t][NG + g]);
-            w0 = pr[t][0] * s0;
-            w1 = pr[t][1] * s1;
-            om[g] = fmaf(pr[t][0], fmaf(-16.0f, s0, bf_hi(vp[t][g])), om[g]);
-            om[g] = fmaf(pr[t][1], fmaf(-16.0f, s1, bf_hi(vp[t][NG + g])), om[g]);
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {                       // truncated to 8 bits each; what is left is exact
-            part[k][t] = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
-            if (k < 2) {
-              w0 -= __uint_as_float(__float_as_uint(w0) & 0xFFFF0000u);
-              w1 -= __uint_as_float(__float_as_uint(w1) & 0xFFFF0000u);
-            }
-          }
-        }
-#pragma unroll
-        for (int wl = 0; wl < 2; ++wl) {
-          const uint32_t y0 = vw[0][2 * g + wl], y1 = vw[1][2 * g + wl];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {                       // dims 64g + 8r + 4wl + 2h, + 1
-            const uint32_t a00 = wide2(h == 0 ? y0 << 3 : y0 >> 5), a10 = wide2(h == 0 ? y0 >> 1 : y0 >> 9);
-            const uint32_t a01 = wide2(h == 0 ? y1 << 3 : y1 >> 5), a11 = wide2(h == 0 ? y1 >> 1 : y1 >> 9);
-            float(&d)[4] = o[4 * g + 2 * wl + h];
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              mma_16816(d, a00, a10, a01, a11, part[k][0], part[k][1], d[0], d[1], d[2], d[3]);
-          }
-        }
-      }
     }
     if (!ok) {                                                // a wait expired: let this warp's own copies land
       if (lane == 0)
@@ -386,6 +498,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     }
 
     // ---- this head's part is read: the warps' states to shared memory
+    const float s_out = s_top * 0x1p-7f;
     l_run += __shfl_xor_sync(kFullMask, l_run, 1);
     l_run += __shfl_xor_sync(kFullMask, l_run, 2);
     if (c == 0) {
@@ -402,8 +515,10 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float(&x0)[4] = o[4 * g + 2 * h], (&x1)[4] = o[4 * g + 2 * h + 1];
-        *reinterpret_cast<float4*>(d0 + 4 * h) = make_float4(x0[0] + v0, x0[2] + v0, x1[0] + v0, x1[2] + v0);
-        *reinterpret_cast<float4*>(d0 + D + 4 * h) = make_float4(x0[1] + v1, x0[3] + v1, x1[1] + v1, x1[3] + v1);
+        *reinterpret_cast<float4*>(d0 + 4 * h) = make_float4(fmaf(x0[0], s_out, v0), fmaf(x0[2], s_out, v0),
+                                                                 fmaf(x1[0], s_out, v0), fmaf(x1[2], s_out, v0));
+        *reinterpret_cast<float4*>(d0 + D + 4 * h) = make_float4(fmaf(x0[1], s_out, v1), fmaf(x0[3], s_out, v1),
+                                                                     fmaf(x1[1], s_out, v1), fmaf(x1[3], s_out, v1));
       }
     }
     const bool failed = __syncthreads_or(!ok);
