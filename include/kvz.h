@@ -433,7 +433,8 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /* j % page_size.  Entries past a head's rows may hold anything.  A page     */
 /* that several entries name may be read by all of them; calls that write    */
 /* need every page they write to be named once.  page_size: a multiple of 16 */
-/* in [16, 1024]; max_pages * page_size <= 2^30; B <= 65535; d in {64, 128}. */
+/* in [16, 1024]; max_pages * page_size <= 2^30; n_pages * page_size < 2^35;  */
+/* B <= 65535; d in {64, 128}.                                               */
 /*                                                                          */
 /* Quantisation, per row and group of 64 dims, in single float32 operations  */
 /* (ties to even): m = min x, step s = bf16((max x - m) * (1/15)) and        */

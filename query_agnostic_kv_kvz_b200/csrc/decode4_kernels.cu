@@ -7,17 +7,18 @@
 // (mma.sync m16n8k16: the G <= 8 queries are below the 64 rows of tcgen05,
 // whose operands would have to be widened into shared or tensor memory first)
 // and the scales are applied to what comes out:
-//   <q, k_j> = sum_groups s_j <q, code_j - 8> + (m_j + 8 s_j) sum(q)
+//   <q, k_j> = sum_groups s_j <q, code_j> + m_j sum(q)
 //   out = sum_groups sum_j (p_j s_j) (code_j - 8) + p_j (m_j + 8 s_j)
-// Two codes of a word widen with one logic instruction, to 1024 + 2^i code
-// (code bits as low mantissa bits), and one fp16 multiply-add, to code - 8.
-// Taking 8 off matters: a sum over many rows of values around 0 is far
-// smaller than the same sum of 0..15, and would drown in the latter's
-// rounding.  The tensor core truncates what it adds to, so it sums 32 rows at
-// a time and the running output adds those in float32.
+// The low 11 bits of an fp16 number count its 2^-24s (subnormal numbers, and
+// the first normal ones that go on from them), so two codes of a word widen
+// with one mask.  V's codes are brought around 0 by one fp16 addition: a sum
+// over many rows of values around 0 is far smaller than the same sum of 0..15,
+// and would drown in the latter's rounding.  The tensor core truncates what it
+// adds to, so it sums 32 rows at a time and the running output adds those in
+// float32.
 //
 // fp16 operands: q is scaled by a power of two to a largest entry of 2^14
-// (bf16's 8 bits stay exact down to 2^-38 of it); a weight p s, scaled by a
+// (bf16's 8 bits stay exact down to 2^-27 of it); a weight p s, scaled by a
 // power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
 // for s), is the sum of two fp16 numbers, 22 bits.
 //
@@ -76,20 +77,25 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
+// The low 11 bits of a small fp16 number count its 2^-24s (exponents 0 and 1
+// join there), so codes masked out of a word are fp16 numbers already; times
+// 2^15 they are normal ones (the tensor core aligns products by exponent
+// fields, and would cut a subnormal operand's short).
+constexpr uint32_t kNormal = 0x78007800u;                     // 2^15, twice
+__device__ __forceinline__ uint32_t normal2(uint32_t w) {
   uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(kNormal));
   return d;
 }
-// Two codes, one in each half of w, as fp16 code - 8 (exact): 1024 + code * 2^SH is
-// scaled by 2^-SH and brought down.  SH is where the codes' four bits start.
+// Two codes, one in each half of w with its four bits from bit SH up, as fp16
+// 2^SH (code - 8) 2^-9.
 template <int SH>
-__device__ __forceinline__ uint32_t wide2(uint32_t w) {
-  static_assert(SH == 0 || SH == 3 || SH == 4, "");
-  constexpr uint32_t mask = 0x000F000Fu << SH;
-  constexpr uint32_t mul = SH == 0 ? 0x3C003C00u : (SH == 3 ? 0x30003000u : 0x2C002C00u);      // 1, 1/8, 1/16
-  constexpr uint32_t add = SH == 0 ? 0xE408E408u : (SH == 3 ? 0xD840D840u : 0xD480D480u);      // -1032, -136, -72
-  return fma_h2((w & mask) | 0x64006400u, mul, add);
+__device__ __forceinline__ uint32_t around0(uint32_t w) {
+  static_assert(SH == 0 || SH == 4, "");
+  constexpr uint32_t mask = 0x000F000Fu << SH, off = SH == 0 ? 0xA400A400u : 0xB400B400u;     // -8 2^-9, -128 2^-9
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w & mask), "r"(kNormal), "r"(off));
+  return d;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t r;
@@ -106,6 +112,12 @@ __device__ __forceinline__ float h_hi(uint32_t w) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h;}" : "=f"(f) : "r"(w));
   return f;
 }
+// 8x8 matrix of 16-bit entries, a row's pair 2c, 2c + 1 in lane (row, c): transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -114,8 +126,10 @@ __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
 
 template <int N>
 __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
-  static_assert(N == 2 || N == 4, "");
-  if constexpr (N == 4) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   } else {
@@ -233,54 +247,53 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     const int n = n_st > warp ? (n_st - warp + kD4Warps - 1) / kD4Warps : 0;
     auto blk_of = [&](int i) -> int { return a0 + 2 * (warp + kD4Warps * i); };
 
-    // lane 0 keeps the ring full
-    const int32_t* const row_pages = p.pg.pages + b * p.pg.max_pages;
-    auto page_ids = [&](int i) -> int2 {
-      if (i >= n) return make_int2(0, 0);
-      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
-      const uint32_t p0 = page_of(p.pg, blk);
-      const uint32_t p1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : p0;
-      return make_int2(__ldg(row_pages + p0), __ldg(row_pages + p1));
+    // The warp keeps its ring full.  Where its stages lie in the pool is looked up
+    // 32 stages at a time, a lane each (block numbers of the stage's two blocks).
+    int at0 = 0, at1 = 0;
+    auto look_up = [&](int i0) {
+      const int i = i0 + lane;
+      if (i < n) {
+        const uint32_t blk = static_cast<uint32_t>(blk_of(i));
+        const uint32_t pi0 = page_of(p.pg, blk);
+        const uint32_t pi1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : pi0;
+        const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(b) * p.pg.max_pages;
+        int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
+        if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
+          report(p.status, KVZ_ERR_INVALID_ARG);              // page 0 stands in, so the read stays inside
+          id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
+          id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
+        }
+        const uint32_t in0 = blk - pi0 * p.pg.blocks;
+        at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(in0);
+        at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
+      }
     };
-    auto valid_id = [&](int id) -> int64_t {                  // page 0 stands in, so the read stays inside
-      if (id >= 0 && id < p.pg.n_pages) return id;
-      report(p.status, KVZ_ERR_INVALID_ARG);
-      return 0;
-    };
-    auto issue = [&](int i, uint32_t ahead, int2 id) {        // `ahead`: how far past the stage now taken
-      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
-      const uint32_t p0 = page_of(p.pg, blk), in0 = blk - p0 * p.pg.blocks;
-      const uint32_t st = (used + ahead) % kD4Stages;
-      uint8_t* dst = ring + st * S::STAGE;
-      const uint8_t* src0 = p.pg.cache + (valid_id(id.x) * p.pg.blocks + in0) * L::BLOCK;
-      const bool two = static_cast<int>(blk) + 1 < a1;
-      mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
-      if (two && in0 + 1 < p.pg.blocks) {
-        bulk_load(dst, src0, 2 * L::BLOCK, &bar[st]);
-      } else {
-        bulk_load(dst, src0, L::BLOCK, &bar[st]);
-        if (two) bulk_load(dst + L::BLOCK, p.pg.cache + valid_id(id.y) * p.pg.blocks * L::BLOCK, L::BLOCK, &bar[st]);
+    auto issue = [&](int i, uint32_t ahead) {                 // `ahead`: how far past the stage now taken
+      const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
+      if (lane == 0) {
+        const uint32_t st = (used + ahead) % kD4Stages;
+        uint8_t* dst = ring + st * S::STAGE;
+        const bool two = blk_of(i) + 1 < a1, joined = two && from1 == from0 + 1;
+        mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
+        bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
+        if (two && !joined)
+          bulk_load(dst + L::BLOCK, p.pg.cache + static_cast<int64_t>(from1) * L::BLOCK, L::BLOCK, &bar[st]);
       }
     };
     __syncthreads();                                          // barriers are initialised; s_o of the last part is read
-    int2 id_next = make_int2(0, 0);
-    if (lane == 0) {
-      int2 id[kD4Stages];
+    look_up(0);
 #pragma unroll
-      for (int i = 0; i < kD4Stages; ++i) id[i] = page_ids(i);
-      id_next = page_ids(kD4Stages);
-#pragma unroll
-      for (int i = 0; i < kD4Stages; ++i)
-        if (i < n) issue(i, i, id[i]);
-    }
+    for (int i = 0; i < kD4Stages; ++i)
+      if (i < n) issue(i, i);                                 // warp-uniform
 
-    // Q fragments (rows = queries; rows >= G are zero), scaled by a power of two
-    // to a largest exponent of 14, and sum(q) per group
-    uint32_t qa[S::KS][2];
-    float qs[NG], c2;
+    // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
+    // two to a largest exponent of 14; lane (r, c) loads query r and then works on
+    // queries 2c, 2c + 1, so it takes their factor and sum(q) per group from there
+    uint32_t qb[S::KS][2];
+    float qs[NG][2], c2[2];
     {
       uint4 v[NG][2];
-      uint32_t ef = 0;                                        // largest exponent field of the row
+      uint32_t ef = 0;                                        // largest exponent field of the query
 #pragma unroll
       for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -295,8 +308,10 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       ef = max(ef, __shfl_xor_sync(kFullMask, ef, 2));
       // an infinity or NaN stays one whatever the factor; an exponent below -112 needs no more than 2^126
       const uint32_t fe = ef == 255u || ef == 0u ? 127u : min(268u - ef, 253u);
-      const float f = __uint_as_float(fe << 23);
-      c2 = p.c2 * __uint_as_float((254u - fe) << 23);
+      const float f = __uint_as_float(fe << 23), back = p.c2 * __uint_as_float((254u - fe) << 23);
+      constexpr float unit = 0x1p-6f;                         // 8 * 2^-9: what one code counts in the products
+      c2[0] = __shfl_sync(kFullMask, back, 8 * c) * (1.0f / unit);
+      c2[1] = __shfl_sync(kFullMask, back, 8 * c + 4) * (1.0f / unit);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = 0.0f;
@@ -306,24 +321,26 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float x0 = bf_lo(w[k]) * f, x1 = bf_hi(w[k]) * f;
-            qa[4 * g + 2 * u + k / 2][k % 2] = pack_h2(x0, x1);
+            constexpr float form[2] = {1.0f, 0.0625f};        // the codes these dims meet are 8- and 128-fold
+            qb[4 * g + 2 * u + k / 2][k % 2] = pack_h2(x0 * form[k % 2], x1 * form[k % 2]);
             sum += x0 + x1;
           }
         }
         sum += __shfl_xor_sync(kFullMask, sum, 1);
         sum += __shfl_xor_sync(kFullMask, sum, 2);
-        qs[g] = sum;
+        qs[g][0] = __shfl_sync(kFullMask, sum, 8 * c) * unit;
+        qs[g][1] = __shfl_sync(kFullMask, sum, 8 * c + 4) * unit;
       }
     }
 
     float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
 #pragma unroll
     for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
-    float m_ref = -INFINITY, thr = -INFINITY;                 // of query r
-    float l_run = 0.0f;                                       // of query r, this lane's keys
-    float om[NG];                                             // sum of p (m + 8 s), the same
+    float m_ref[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // of queries 2c, 2c + 1
+    float l_run[2] = {0.0f, 0.0f};                            // of the same, this lane's keys
+    float om[NG][2];                                          // sum of p (m + 8 s), the same
 #pragma unroll
-    for (int g = 0; g < NG; ++g) om[g] = 0.0f;
+    for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
     float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
 
     bool ok = true;
@@ -337,80 +354,67 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       // lies past them, in the page or left in the stage, has no influence)
       const int rows = min(count - blk0 * kC4Rows, (a1 - blk0) * kC4Rows);
 
-      // ---- scores of query r and keys 16k + 8t + 2c + e of the stage
-      float x[2][2][2];
-      uint32_t vp[2][2][2 * NG];                              // V scales of the same keys
-      uint32_t vmax = 0u;
+      // ---- scores of keys 16k + 8h + r of the stage and queries 2c + e
+      float x[2][2][2];                                       // [k][h][e]
+      uint32_t vp[2][2][NG];                                  // V scales of those keys
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        __syncwarp();                                         // keeps the next block's loads (and registers) behind this one's use
+        const uint8_t* blk = stage + k * L::BLOCK;
+        uint32_t kw[2][2 * NG], kp[2][NG];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint8_t* blk = stage + k * L::BLOCK;
-          uint32_t kw[2 * NG], kp[2 * NG];
-          lds_words(blk + (8 * t + r) * (D / 2) + c * (8 * NG), kw);
-          lds_words(blk + L::KS_OFF + (8 * t + 2 * c) * (4 * NG), kp);
-          lds_words(blk + L::VS_OFF + (8 * t + 2 * c) * (4 * NG), vp[k][t]);
-          x[k][t][0] = x[k][t][1] = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+          lds_words(blk + (8 * h + r) * (D / 2) + c * (8 * NG), kw[h]);
+          lds_words(blk + L::KS_OFF + (8 * h + r) * (4 * NG), kp[h]);
+          lds_words(blk + L::VS_OFF + (8 * h + r) * (4 * NG), vp[k][h]);
+          x[k][h][0] = x[k][h][1] = 0.0f;
+        }
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            float acc[4];
-            const float init = 8.0f * qs[g];
+        for (int g = 0; g < NG; ++g) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t w = kw[2 * g + u], w7 = w >> 7;
-              const uint32_t(&q0)[2] = qa[4 * g + 2 * u], (&q1)[2] = qa[4 * g + 2 * u + 1];
-              if (u == 0)
-                mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2<3>(w), wide2<0>(w7), init, init, 0.0f, 0.0f);
-              else
-                mma_16816(acc, q0[0], 0u, q0[1], 0u, wide2<3>(w), wide2<0>(w7), acc[0], acc[1], acc[2], acc[3]);
-              mma_16816(acc, q1[0], 0u, q1[1], 0u, wide2<4>(w7), wide2<3>(__funnelshift_r(w, w, 12)), acc[0], acc[1],
-                        acc[2], acc[3]);
-            }
+          for (int u = 0; u < 2; ++u) {
+            // nibbles 0, 4 and 1, 5 of the rotated words, then 2, 6 and 3, 7: bits 3..6 and 7..10 of either half
+            const uint32_t w0 = kw[0][2 * g + u], w1 = kw[1][2 * g + u];
+            const uint32_t y0 = __funnelshift_r(w0, w0, 8), y1 = __funnelshift_r(w1, w1, 8);
+            constexpr uint32_t lo = 0x00780078u, hi = 0x07800780u;
+            const uint32_t(&q0)[2] = qb[4 * g + 2 * u], (&q1)[2] = qb[4 * g + 2 * u + 1];
+            mma_16816(acc, normal2(w0 & lo), normal2(w1 & lo), normal2(w0 & hi), normal2(w1 & hi), q0[0], q0[1], acc[0],
+                      acc[1], acc[2], acc[3]);
+            mma_16816(acc, normal2(y0 & lo), normal2(y1 & lo), normal2(y0 & hi), normal2(y1 & hi), q1[0], q1[1], acc[0],
+                      acc[1], acc[2], acc[3]);
+          }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t sm = kp[e * NG + g];
-              x[k][t][e] = fmaf(bf_lo(sm), acc[e], fmaf(bf_hi(sm), qs[g], x[k][t][e]));
-            }
+          for (int h = 0; h < 2; ++h) {
+            const float s = bf_lo(kp[h][g]), m = bf_hi(kp[h][g]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[k][h][e] = fmaf(s, acc[2 * h + e], fmaf(m, qs[g][e], x[k][h][e]));
           }
         }
+      }
       if (rows < 2 * kC4Rows) {                               // warp-uniform
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int h = 0; h < 2; ++h)
+            if (16 * k + 8 * h + r >= rows) {
+              x[k][h][0] = x[k][h][1] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (16 * k + 8 * t + 2 * c + e >= rows) {
-                x[k][t][e] = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) vp[k][t][e * NG + g] = 0u;
-              }
+              for (int g = 0; g < NG; ++g) vp[k][h][g] = 0u;
+            }
       }
+      // ---- softmax against references that move only when a logit passes them by 2^7; the steps' scale likewise
+      float xm[2];
+      uint32_t vmax = 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) xm[e] = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int w = 0; w < 2 * NG; ++w) vmax = max_bf2(vmax, vp[k][t][w]);
-      // ---- softmax against a reference that moves only when a logit passes it by 2^7; the steps' scale likewise
-      float xm = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) xm = fmaxf(xm, fmaxf(x[k][t][0], x[k][t][1]));
-      if (__any_sync(kFullMask, xm > thr || bf_lo(vmax) > s_top)) {
-        float mx = fmaxf(xm, __shfl_xor_sync(kFullMask, xm, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
-        const bool up = mx > thr;
-        const float mn = up ? mx * c2 : m_ref;
-        const float alpha = up ? ex2(m_ref - mn) : 1.0f;      // 0 the first time
-        if (up) {
-          m_ref = mn;
-          thr = (mn + kD4Slack) / c2;
-          l_run *= alpha;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) om[g] *= alpha;
-        }
+          for (int g = 0; g < NG; ++g) vmax = max_bf2(vmax, vp[k][h][g]);
+      if (__any_sync(kFullMask, xm[0] > thr[0] || xm[1] > thr[1] || bf_lo(vmax) > s_top)) {
         // the power of two past the largest step (at least 2^-100, at most 2^126), twice that for room
         const uint32_t top = __reduce_max_sync(kFullMask, __float_as_uint(bf_lo(vmax)));
         float beta = 1.0f;
@@ -421,47 +425,65 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
           s_top = s_new;
           s_mul = __uint_as_float((254u + 7u - e2) << 23);
         }
-        const float al0 = __shfl_sync(kFullMask, alpha, 8 * c) * beta;
-        const float al1 = __shfl_sync(kFullMask, alpha, 8 * c + 4) * beta;
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = xm[e];
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
+          al[e] = 1.0f;
+          if (mx > thr[e]) {
+            const float mn = mx * c2[e];
+            al[e] = ex2(m_ref[e] - mn);                       // 0 the first time
+            m_ref[e] = mn;
+            thr[e] = (mn + kD4Slack) / c2[e];
+            l_run[e] *= al[e];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) om[g][e] *= al[e];
+          }
+          al[e] *= beta;
+        }
 #pragma unroll
         for (int t = 0; t < S::MT; ++t) {
-          o[t][0] *= al0, o[t][1] *= al1;
-          o[t][2] *= al0, o[t][3] *= al1;
+          o[t][0] *= al[0], o[t][1] *= al[1];
+          o[t][2] *= al[0], o[t][3] *= al[1];
         }
       }
-      float pr[2][2][2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            pr[k][t][e] = ex2(fmaf(x[k][t][e], c2, -m_ref));
-            l_run += pr[k][t][e];
+            x[k][h][e] = ex2(fmaf(x[k][h][e], c2[e], -m_ref[e]));   // the weight p
+            l_run[e] += x[k][h][e];
           }
 
       // ---- out^T += V^T (p s)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
+        uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float s = bf_lo(vp[k][h][g]), m8 = fmaf(8.0f, s, bf_hi(vp[k][h][g])), sx = s * s_mul;
+            const float p0 = x[k][h][0], p1 = x[k][h][1];
+            om[g][0] = fmaf(p0, m8, om[g][0]);
+            om[g][1] = fmaf(p1, m8, om[g][1]);
+            const float w0 = p0 * sx, w1 = p1 * sx;
+            const uint32_t w = pack_h2(w0, w1);
+            hi[k][h] = transpose8(w);
+            lo[k][h] = transpose8(pack_h2(w0 - h_lo(w), w1 - h_hi(w)));
+          }
+        __syncwarp();
         uint32_t vw[2][2][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             lds_words(stage + k * L::BLOCK + L::V_OFF + (4 * t + c) * D + (r * NG + g) * 8, vw[k][t]);
-        uint32_t hi[2][2], lo[2][2];                          // the weights p s 2^(7 - E) = hi + lo
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float s0 = bf_lo(vp[k][t][g]), s1 = bf_lo(vp[k][t][NG + g]);
-            const float p0 = pr[k][t][0], p1 = pr[k][t][1];
-            om[g] = fmaf(p0, fmaf(8.0f, s0, bf_hi(vp[k][t][g])), om[g]);
-            om[g] = fmaf(p1, fmaf(8.0f, s1, bf_hi(vp[k][t][NG + g])), om[g]);
-            const float w0 = p0 * (s0 * s_mul), w1 = p1 * (s1 * s_mul);
-            hi[k][t] = pack_h2(w0, w1);
-            lo[k][t] = pack_h2(w0 - h_lo(hi[k][t]), w1 - h_hi(hi[k][t]));
-          }
 #pragma unroll
         for (int wl = 0; wl < 2; ++wl)
 #pragma unroll
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
             for (int k = 0; k < 2; ++k) {
               uint32_t y0 = vw[k][0][wl], y1 = vw[k][1][wl];
               if (h == 1) y0 >>= 8, y1 >>= 8;
-              a[k][0] = wide2<0>(y0), a[k][1] = wide2<4>(y0), a[k][2] = wide2<0>(y1), a[k][3] = wide2<4>(y1);
+              a[k][0] = around0<0>(y0), a[k][1] = around0<4>(y0), a[k][2] = around0<0>(y1), a[k][3] = around0<4>(y1);
             }
             float d[4];
             mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1], 0.0f, 0.0f, 0.0f, 0.0f);
@@ -484,10 +506,9 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
           }
       }
       __syncwarp();
-      if (lane == 0 && i + kD4Stages < n) {                   // the stage is read: refill it
-        const int2 id = id_next;
-        id_next = page_ids(i + kD4Stages + 1);
-        issue(i + kD4Stages, kD4Stages, id);
+      if (i + kD4Stages < n) {                                // the stage is read: refill it
+        if (((i + kD4Stages) & 31) == 0) look_up(i + kD4Stages);
+        issue(i + kD4Stages, kD4Stages);
       }
       ++used;
     }
@@ -498,27 +519,30 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     }
 
     // ---- this head's part is read: the warps' states to shared memory
-    const float s_out = s_top * 0x1p-7f;
-    l_run += __shfl_xor_sync(kFullMask, l_run, 1);
-    l_run += __shfl_xor_sync(kFullMask, l_run, 2);
-    if (c == 0) {
-      s_m[warp][r] = m_ref;
-      s_l[warp][r] = l_run;
-    }
+    const float s_out = s_top * 0x1p2f;                       // 2^E 2^-7 2^9
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      float v = om[g];
-      v += __shfl_xor_sync(kFullMask, v, 1);
-      v += __shfl_xor_sync(kFullMask, v, 2);
-      const float v0 = __shfl_sync(kFullMask, v, 8 * c), v1 = __shfl_sync(kFullMask, v, 8 * c + 4);
-      float* d0 = s_o + (warp * 8 + 2 * c) * D + 64 * g + 8 * r;
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float(&x0)[4] = o[4 * g + 2 * h], (&x1)[4] = o[4 * g + 2 * h + 1];
-        *reinterpret_cast<float4*>(d0 + 4 * h) = make_float4(fmaf(x0[0], s_out, v0), fmaf(x0[2], s_out, v0),
-                                                                 fmaf(x1[0], s_out, v0), fmaf(x1[2], s_out, v0));
-        *reinterpret_cast<float4*>(d0 + D + 4 * h) = make_float4(fmaf(x0[1], s_out, v1), fmaf(x0[3], s_out, v1),
-                                                                     fmaf(x1[1], s_out, v1), fmaf(x1[3], s_out, v1));
+      for (int sh = 4; sh < 32; sh <<= 1) {
+        l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], sh);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) om[g][e] += __shfl_xor_sync(kFullMask, om[g][e], sh);
+      }
+      if (r == 0) {
+        s_m[warp][2 * c + e] = m_ref[e];
+        s_l[warp][2 * c + e] = l_run[e];
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float* d0 = s_o + (warp * 8 + 2 * c + e) * D + 64 * g + 8 * r;
+#pragma unroll
+        for (int wl = 0; wl < 2; ++wl) {
+          const float(&x0)[4] = o[4 * g + 2 * wl], (&x1)[4] = o[4 * g + 2 * wl + 1];
+          // odd dims' codes were taken 16-fold
+          *reinterpret_cast<float4*>(d0 + 4 * wl) =
+              make_float4(fmaf(x0[e], s_out, om[g][e]), fmaf(x0[2 + e], s_out * 0.0625f, om[g][e]),
+                          fmaf(x1[e], s_out, om[g][e]), fmaf(x1[2 + e], s_out * 0.0625f, om[g][e]));
+        }
       }
     }
     const bool failed = __syncthreads_or(!ok);

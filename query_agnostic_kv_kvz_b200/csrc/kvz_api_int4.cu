@@ -26,6 +26,7 @@ kvz_status check_pages(const void* cache, int64_t n_pages, int page_size, const 
   if (page_size < 16 || page_size > 1024 || page_size % 16 != 0) return KVZ_ERR_UNSUPPORTED;
   if (B < 1 || B > 65535 || n_pages < 1 || n_pages > 0x7FFFFFFF || max_pages < 1) return KVZ_ERR_INVALID_ARG;
   if (max_pages > kMaxCacheRows / page_size) return KVZ_ERR_INVALID_ARG;
+  if (n_pages > 0x7FFFFFFF / (page_size / 16)) return KVZ_ERR_INVALID_ARG;   // a pool's blocks are numbered in 31 bits
   if (!aligned(cache, 16) || !aligned(pages, 4)) return KVZ_ERR_ALIGNMENT;
   pg->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   pg->n_pages = n_pages;
