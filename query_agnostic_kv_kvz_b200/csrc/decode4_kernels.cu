@@ -33,6 +33,7 @@
 // warps merge in shared memory at the end of each head's part.  A head that
 // several CTAs read leaves one partial per CTA, which a second launch joins
 // in order: no atomics, and identical inputs give identical results.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -42,6 +43,8 @@
 #include "kvz_internal.h"
 #include "kvz_sm100.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace kvz {
 
 namespace {
@@ -50,6 +53,10 @@ constexpr int kD4Warps = 8;
 constexpr int kD4Threads = kD4Warps * 32;
 constexpr int kD4Stages = 2;
 constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share is at least a stage per warp
+#ifndef KVZ_D4_CLUSTER_ROWS
+#define KVZ_D4_CLUSTER_ROWS 1024
+#endif
+constexpr int kD4ClusterRows = KVZ_D4_CLUSTER_ROWS;           // rows a CTA may have to read in the cluster form
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
 
@@ -78,15 +85,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 // The low 11 bits of a small fp16 number count its 2^-24s (exponents 0 and 1
-// join there), so codes masked out of a word are fp16 numbers already; times
-// 2^15 they are normal ones (the tensor core aligns products by exponent
-// fields, and would cut a subnormal operand's short).
+// join there), so codes masked out of a word are fp16 numbers already.  V's,
+// times 2^15, are normal ones: the tensor core aligns products by exponent
+// fields and cuts a subnormal operand's short, which costs a sum of thousands
+// of rows 4 of its bits, a logit's 128 products nothing that its rounding to
+// float32 does not.
 constexpr uint32_t kNormal = 0x78007800u;                     // 2^15, twice
-__device__ __forceinline__ uint32_t normal2(uint32_t w) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(kNormal));
-  return d;
-}
 // Two codes, one in each half of w with its four bits from bit SH up, as fp16
 // 2^SH (code - 8) 2^-9.
 template <int SH>
@@ -153,11 +157,348 @@ __device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* s_red) {
   return t;
 }
 
+// One part of a head, blocks [a0, a1) of head b's `count` rows, read by the
+// CTA's warps 32 rows at a time; each leaves its reference, sum and output per
+// query in shared memory.  False in a warp whose wait expired.
 template <int D>
-__global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) {
+__device__ __forceinline__ bool read_part(const Dec4Args& p, int64_t b, int count, int a0, int a1, uint8_t* ring,
+                                          uint64_t* bar, uint32_t& used, volatile int* abort_flag, float* s_o,
+                                          float (*s_m)[8], float (*s_l)[8]) {
   using L = C4<D>;
   using S = D4<D>;
   constexpr int NG = L::NG;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int G = p.G;
+  const int n_st = (a1 - a0 + 1) / 2;                       // 32-row stages of this part; warp w takes w, w + 8, ...
+  const int n = n_st > warp ? (n_st - warp + kD4Warps - 1) / kD4Warps : 0;
+  auto blk_of = [&](int i) -> int { return a0 + 2 * (warp + kD4Warps * i); };
+
+  // The warp keeps its ring full.  Where its stages lie in the pool is looked up
+  // 32 stages at a time, a lane each (block numbers of the stage's two blocks).
+  int at0 = 0, at1 = 0;
+  auto look_up = [&](int i0) {
+    const int i = i0 + lane;
+    if (i < n) {
+      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
+      const uint32_t pi0 = page_of(p.pg, blk);
+      const uint32_t pi1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : pi0;
+      const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(b) * p.pg.max_pages;
+      int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
+      if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
+        report(p.status, KVZ_ERR_INVALID_ARG);              // page 0 stands in, so the read stays inside
+        id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
+        id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
+      }
+      const uint32_t in0 = blk - pi0 * p.pg.blocks;
+      at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(in0);
+      at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
+    }
+  };
+  auto issue = [&](int i, uint32_t ahead) {                 // `ahead`: how far past the stage now taken
+    const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
+    if (lane == 0) {
+      const uint32_t st = (used + ahead) % kD4Stages;
+      uint8_t* dst = ring + st * S::STAGE;
+      const bool two = blk_of(i) + 1 < a1, joined = two && from1 == from0 + 1;
+      mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
+      bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
+      if (two && !joined)
+        bulk_load(dst + L::BLOCK, p.pg.cache + static_cast<int64_t>(from1) * L::BLOCK, L::BLOCK, &bar[st]);
+    }
+  };
+  __syncthreads();                                          // barriers are initialised; s_o of the last part is read
+  look_up(0);
+#pragma unroll
+  for (int i = 0; i < kD4Stages; ++i)
+    if (i < n) issue(i, i);                                 // warp-uniform
+
+  // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
+  // two to a largest exponent of 14; lane (r, c) loads query r and then works on
+  // queries 2c, 2c + 1, so it takes their factor and sum(q) per group from there
+  uint32_t qb[S::KS][2];
+  float qs[NG][2], c2[2];
+  {
+    uint4 v[NG][2];
+    uint32_t ef = 0;                                        // largest exponent field of the query
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        v[g][u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
+        const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
+      }
+    ef = max(ef, __shfl_xor_sync(kFullMask, ef, 1));
+    ef = max(ef, __shfl_xor_sync(kFullMask, ef, 2));
+    // an infinity or NaN stays one whatever the factor; an exponent below -112 needs no more than 2^126
+    const uint32_t fe = ef == 255u || ef == 0u ? 127u : min(268u - ef, 253u);
+    const float f = __uint_as_float(fe << 23), back = p.c2 * __uint_as_float((254u - fe) << 23);
+    constexpr float unit = 0x1p-21f;                        // 8 * 2^-24: what one code counts in the products
+    c2[0] = __shfl_sync(kFullMask, back, 8 * c) * (1.0f / unit);
+    c2[1] = __shfl_sync(kFullMask, back, 8 * c + 4) * (1.0f / unit);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x0 = bf_lo(w[k]) * f, x1 = bf_hi(w[k]) * f;
+          constexpr float form[2] = {1.0f, 0.0625f};        // the codes these dims meet are 8- and 128-fold
+          qb[4 * g + 2 * u + k / 2][k % 2] = pack_h2(x0 * form[k % 2], x1 * form[k % 2]);
+          sum += x0 + x1;
+        }
+      }
+      sum += __shfl_xor_sync(kFullMask, sum, 1);
+      sum += __shfl_xor_sync(kFullMask, sum, 2);
+      qs[g][0] = __shfl_sync(kFullMask, sum, 8 * c) * unit;
+      qs[g][1] = __shfl_sync(kFullMask, sum, 8 * c + 4) * unit;
+    }
+  }
+
+  float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+  float m_ref[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // of queries 2c, 2c + 1
+  float l_run[2] = {0.0f, 0.0f};                            // of the same, this lane's keys
+  float om[NG][2];                                          // sum of p (m + 8 s), the same
+#pragma unroll
+  for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
+  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
+
+  bool ok = true;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t st = used % kD4Stages;
+    ok = mbar_wait_warp(&bar[st], (used / kD4Stages) & 1u, abort_flag, p.status);
+    if (!ok) break;                                         // warp-uniform
+    const uint8_t* stage = ring + st * S::STAGE;
+    const int blk0 = blk_of(i);
+    // rows of the stage that count: the head may end inside it, and this CTA's share after its first block (what
+    // lies past them, in the page or left in the stage, has no influence)
+    const int rows = min(count - blk0 * kC4Rows, (a1 - blk0) * kC4Rows);
+
+    // ---- scores of keys 16k + 8h + r of the stage and queries 2c + e
+    float x[2][2][2];                                       // [k][h][e]
+    uint32_t vp[2][2][NG];                                  // V scales of those keys
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      __syncwarp();                                         // keeps the next block's loads (and registers) behind this one's use
+      const uint8_t* blk = stage + k * L::BLOCK;
+      uint32_t kw[2][2 * NG], kp[2][NG];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lds_words(blk + (8 * h + r) * (D / 2) + c * (8 * NG), kw[h]);
+        lds_words(blk + L::KS_OFF + (8 * h + r) * (4 * NG), kp[h]);
+        lds_words(blk + L::VS_OFF + (8 * h + r) * (4 * NG), vp[k][h]);
+        x[k][h][0] = x[k][h][1] = 0.0f;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          // nibbles 0, 4 and 1, 5 of the rotated words, then 2, 6 and 3, 7: bits 3..6 and 7..10 of either half
+          const uint32_t w0 = kw[0][2 * g + u], w1 = kw[1][2 * g + u];
+          const uint32_t y0 = __funnelshift_r(w0, w0, 8), y1 = __funnelshift_r(w1, w1, 8);
+          constexpr uint32_t lo = 0x00780078u, hi = 0x07800780u;
+          const uint32_t(&q0)[2] = qb[4 * g + 2 * u], (&q1)[2] = qb[4 * g + 2 * u + 1];
+          mma_16816(acc, w0 & lo, w1 & lo, w0 & hi, w1 & hi, q0[0], q0[1], acc[0], acc[1], acc[2], acc[3]);
+          mma_16816(acc, y0 & lo, y1 & lo, y0 & hi, y1 & hi, q1[0], q1[1], acc[0], acc[1], acc[2], acc[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = bf_lo(kp[h][g]), m = bf_hi(kp[h][g]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[k][h][e] = fmaf(s, acc[2 * h + e], fmaf(m, qs[g][e], x[k][h][e]));
+        }
+      }
+    }
+    if (rows < 2 * kC4Rows) {                               // warp-uniform
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (16 * k + 8 * h + r >= rows) {
+            x[k][h][0] = x[k][h][1] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) vp[k][h][g] = 0u;
+          }
+    }
+    // ---- softmax against references that move only when a logit passes them by 2^7; the steps' scale likewise
+    float xm[2];
+    uint32_t vmax = 0u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) xm[e] = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) vmax = max_bf2(vmax, vp[k][h][g]);
+    if (__any_sync(kFullMask, xm[0] > thr[0] || xm[1] > thr[1] || bf_lo(vmax) > s_top)) {
+      // the power of two past the largest step (at least 2^-100, at most 2^126), twice that for room
+      const uint32_t top = __reduce_max_sync(kFullMask, __float_as_uint(bf_lo(vmax)));
+      float beta = 1.0f;
+      if (__uint_as_float(top) > s_top) {
+        const uint32_t e2 = min(max((top >> 23) + 2u, 27u), 253u);
+        const float s_new = __uint_as_float(e2 << 23);
+        beta = s_top / s_new;                               // 0 the first time
+        s_top = s_new;
+        s_mul = __uint_as_float((254u + 7u - e2) << 23);
+      }
+      float al[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = xm[e];
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
+        al[e] = 1.0f;
+        if (mx > thr[e]) {
+          const float mn = mx * c2[e];
+          al[e] = ex2(m_ref[e] - mn);                       // 0 the first time
+          m_ref[e] = mn;
+          thr[e] = (mn + kD4Slack) / c2[e];
+          l_run[e] *= al[e];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) om[g][e] *= al[e];
+        }
+        al[e] *= beta;
+      }
+#pragma unroll
+      for (int t = 0; t < S::MT; ++t) {
+        o[t][0] *= al[0], o[t][1] *= al[1];
+        o[t][2] *= al[0], o[t][3] *= al[1];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[k][h][e] = ex2(fmaf(x[k][h][e], c2[e], -m_ref[e]));   // the weight p
+          l_run[e] += x[k][h][e];
+        }
+
+    // ---- out^T += V^T (p s)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
+      uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = bf_lo(vp[k][h][g]), m8 = fmaf(8.0f, s, bf_hi(vp[k][h][g])), sx = s * s_mul;
+          const float p0 = x[k][h][0], p1 = x[k][h][1];
+          om[g][0] = fmaf(p0, m8, om[g][0]);
+          om[g][1] = fmaf(p1, m8, om[g][1]);
+          const float w0 = p0 * sx, w1 = p1 * sx;
+          const uint32_t w = pack_h2(w0, w1);
+          hi[k][h] = transpose8(w);
+          lo[k][h] = transpose8(pack_h2(w0 - h_lo(w), w1 - h_hi(w)));
+        }
+      __syncwarp();
+      uint32_t vw[2][2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          lds_words(stage + k * L::BLOCK + L::V_OFF + (4 * t + c) * D + (r * NG + g) * 8, vw[k][t]);
+#pragma unroll
+      for (int wl = 0; wl < 2; ++wl)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                       // dims 64g + 8r + 4wl + 2h, + 1
+          uint32_t a[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t y0 = vw[k][0][wl], y1 = vw[k][1][wl];
+            if (h == 1) y0 >>= 8, y1 >>= 8;
+            a[k][0] = around0<0>(y0), a[k][1] = around0<4>(y0), a[k][2] = around0<0>(y1), a[k][3] = around0<4>(y1);
+          }
+          float d[4];
+          mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+          mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1], d[0], d[1], d[2], d[3]);
+          mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], hi[0][0], hi[0][1], d[0], d[1], d[2], d[3]);
+          mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], hi[1][0], hi[1][1], d[0], d[1], d[2], d[3]);
+          float(&acc)[4] = o[4 * g + 2 * wl + h];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] += d[j];
+        }
+    }
+    __syncwarp();
+    if (i + kD4Stages < n) {                                // the stage is read: refill it
+      if (((i + kD4Stages) & 31) == 0) look_up(i + kD4Stages);
+      issue(i + kD4Stages, kD4Stages);
+    }
+    ++used;
+  }
+  if (!ok) {                                                // a wait expired: let this warp's own copies land
+    if (lane == 0)
+      for (int i = 0; i < kD4Stages; ++i) mbar_wait_for(&bar[(used + i) % kD4Stages], ((used + i) / kD4Stages) & 1u,
+                                                        20000000ull);
+  }
+
+  // ---- this head's part is read: the warps' states to shared memory
+  const float s_out = s_top * 0x1p2f;                       // 2^E 2^-7 2^9
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) {
+      l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], sh);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) om[g][e] += __shfl_xor_sync(kFullMask, om[g][e], sh);
+    }
+    if (r == 0) {
+      s_m[warp][2 * c + e] = m_ref[e];
+      s_l[warp][2 * c + e] = l_run[e];
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float* d0 = s_o + (warp * 8 + 2 * c + e) * D + 64 * g + 8 * r;
+#pragma unroll
+      for (int wl = 0; wl < 2; ++wl) {
+        const float(&x0)[4] = o[4 * g + 2 * wl], (&x1)[4] = o[4 * g + 2 * wl + 1];
+        // odd dims' codes were taken 16-fold
+        *reinterpret_cast<float4*>(d0 + 4 * wl) =
+            make_float4(fmaf(x0[e], s_out, om[g][e]), fmaf(x0[2 + e], s_out * 0.0625f, om[g][e]),
+                        fmaf(x1[e], s_out, om[g][e]), fmaf(x1[2 + e], s_out * 0.0625f, om[g][e]));
+      }
+    }
+  }
+  return ok;
+}
+
+// The warps' states of query g joined, for the four dims from 4 e4 on (of the
+// G * D): reference M, sum, output relative to M.
+template <int D>
+__device__ __forceinline__ float4 join_warps(int e4, const float* s_o, const float (*s_m)[8], const float (*s_l)[8],
+                                             float& M, float& Ls) {
+  const int g = 4 * e4 / D;
+  M = -INFINITY, Ls = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kD4Warps; ++w) M = fmaxf(M, s_m[w][g]);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < kD4Warps; ++w) {
+    const float mw = s_m[w][g], lw = s_l[w][g];
+    const bool none = mw == -INFINITY && lw == 0.0f;          // the warp had no block
+    const float wgt = none ? 0.0f : exp2f(mw - M);
+    const float4 v = *reinterpret_cast<const float4*>(s_o + w * 8 * D + 4 * e4);
+    Ls = fmaf(lw, wgt, Ls);
+    acc.x = fmaf(v.x, wgt, acc.x), acc.y = fmaf(v.y, wgt, acc.y);
+    acc.z = fmaf(v.z, wgt, acc.z), acc.w = fmaf(v.w, wgt, acc.w);
+  }
+  return acc;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) {
+  using S = D4<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kD4Warps * kD4Stages];
   __shared__ int s_abort;
@@ -166,7 +507,6 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   __shared__ int64_t s_find[2];                               // head that holds the first block, its first block
   __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = lane >> 2, c = lane & 3;
   const int G = p.G;
   volatile int* abort_flag = &s_abort;
 
@@ -243,308 +583,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     const int64_t n_blk = blocks_of(count, p.cap);
     const int a0 = static_cast<int>(u0 > start ? u0 - start : 0);
     const int a1 = static_cast<int>(u1 - start < n_blk ? u1 - start : n_blk);
-    const int n_st = (a1 - a0 + 1) / 2;                       // 32-row stages of this part; warp w takes w, w + 8, ...
-    const int n = n_st > warp ? (n_st - warp + kD4Warps - 1) / kD4Warps : 0;
-    auto blk_of = [&](int i) -> int { return a0 + 2 * (warp + kD4Warps * i); };
-
-    // The warp keeps its ring full.  Where its stages lie in the pool is looked up
-    // 32 stages at a time, a lane each (block numbers of the stage's two blocks).
-    int at0 = 0, at1 = 0;
-    auto look_up = [&](int i0) {
-      const int i = i0 + lane;
-      if (i < n) {
-        const uint32_t blk = static_cast<uint32_t>(blk_of(i));
-        const uint32_t pi0 = page_of(p.pg, blk);
-        const uint32_t pi1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : pi0;
-        const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(b) * p.pg.max_pages;
-        int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
-        if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
-          report(p.status, KVZ_ERR_INVALID_ARG);              // page 0 stands in, so the read stays inside
-          id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
-          id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
-        }
-        const uint32_t in0 = blk - pi0 * p.pg.blocks;
-        at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(in0);
-        at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
-      }
-    };
-    auto issue = [&](int i, uint32_t ahead) {                 // `ahead`: how far past the stage now taken
-      const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
-      if (lane == 0) {
-        const uint32_t st = (used + ahead) % kD4Stages;
-        uint8_t* dst = ring + st * S::STAGE;
-        const bool two = blk_of(i) + 1 < a1, joined = two && from1 == from0 + 1;
-        mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
-        bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
-        if (two && !joined)
-          bulk_load(dst + L::BLOCK, p.pg.cache + static_cast<int64_t>(from1) * L::BLOCK, L::BLOCK, &bar[st]);
-      }
-    };
-    __syncthreads();                                          // barriers are initialised; s_o of the last part is read
-    look_up(0);
-#pragma unroll
-    for (int i = 0; i < kD4Stages; ++i)
-      if (i < n) issue(i, i);                                 // warp-uniform
-
-    // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
-    // two to a largest exponent of 14; lane (r, c) loads query r and then works on
-    // queries 2c, 2c + 1, so it takes their factor and sum(q) per group from there
-    uint32_t qb[S::KS][2];
-    float qs[NG][2], c2[2];
-    {
-      uint4 v[NG][2];
-      uint32_t ef = 0;                                        // largest exponent field of the query
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          v[g][u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
-          const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
-        }
-      ef = max(ef, __shfl_xor_sync(kFullMask, ef, 1));
-      ef = max(ef, __shfl_xor_sync(kFullMask, ef, 2));
-      // an infinity or NaN stays one whatever the factor; an exponent below -112 needs no more than 2^126
-      const uint32_t fe = ef == 255u || ef == 0u ? 127u : min(268u - ef, 253u);
-      const float f = __uint_as_float(fe << 23), back = p.c2 * __uint_as_float((254u - fe) << 23);
-      constexpr float unit = 0x1p-6f;                         // 8 * 2^-9: what one code counts in the products
-      c2[0] = __shfl_sync(kFullMask, back, 8 * c) * (1.0f / unit);
-      c2[1] = __shfl_sync(kFullMask, back, 8 * c + 4) * (1.0f / unit);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = bf_lo(w[k]) * f, x1 = bf_hi(w[k]) * f;
-            constexpr float form[2] = {1.0f, 0.0625f};        // the codes these dims meet are 8- and 128-fold
-            qb[4 * g + 2 * u + k / 2][k % 2] = pack_h2(x0 * form[k % 2], x1 * form[k % 2]);
-            sum += x0 + x1;
-          }
-        }
-        sum += __shfl_xor_sync(kFullMask, sum, 1);
-        sum += __shfl_xor_sync(kFullMask, sum, 2);
-        qs[g][0] = __shfl_sync(kFullMask, sum, 8 * c) * unit;
-        qs[g][1] = __shfl_sync(kFullMask, sum, 8 * c + 4) * unit;
-      }
-    }
-
-    float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
-#pragma unroll
-    for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
-    float m_ref[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // of queries 2c, 2c + 1
-    float l_run[2] = {0.0f, 0.0f};                            // of the same, this lane's keys
-    float om[NG][2];                                          // sum of p (m + 8 s), the same
-#pragma unroll
-    for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
-    float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
-
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const uint32_t st = used % kD4Stages;
-      ok = mbar_wait_warp(&bar[st], (used / kD4Stages) & 1u, abort_flag, p.status);
-      if (!ok) break;                                         // warp-uniform
-      const uint8_t* stage = ring + st * S::STAGE;
-      const int blk0 = blk_of(i);
-      // rows of the stage that count: the head may end inside it, and this CTA's share after its first block (what
-      // lies past them, in the page or left in the stage, has no influence)
-      const int rows = min(count - blk0 * kC4Rows, (a1 - blk0) * kC4Rows);
-
-      // ---- scores of keys 16k + 8h + r of the stage and queries 2c + e
-      float x[2][2][2];                                       // [k][h][e]
-      uint32_t vp[2][2][NG];                                  // V scales of those keys
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        __syncwarp();                                         // keeps the next block's loads (and registers) behind this one's use
-        const uint8_t* blk = stage + k * L::BLOCK;
-        uint32_t kw[2][2 * NG], kp[2][NG];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          lds_words(blk + (8 * h + r) * (D / 2) + c * (8 * NG), kw[h]);
-          lds_words(blk + L::KS_OFF + (8 * h + r) * (4 * NG), kp[h]);
-          lds_words(blk + L::VS_OFF + (8 * h + r) * (4 * NG), vp[k][h]);
-          x[k][h][0] = x[k][h][1] = 0.0f;
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            // nibbles 0, 4 and 1, 5 of the rotated words, then 2, 6 and 3, 7: bits 3..6 and 7..10 of either half
-            const uint32_t w0 = kw[0][2 * g + u], w1 = kw[1][2 * g + u];
-            const uint32_t y0 = __funnelshift_r(w0, w0, 8), y1 = __funnelshift_r(w1, w1, 8);
-            constexpr uint32_t lo = 0x00780078u, hi = 0x07800780u;
-            const uint32_t(&q0)[2] = qb[4 * g + 2 * u], (&q1)[2] = qb[4 * g + 2 * u + 1];
-            mma_16816(acc, normal2(w0 & lo), normal2(w1 & lo), normal2(w0 & hi), normal2(w1 & hi), q0[0], q0[1], acc[0],
-                      acc[1], acc[2], acc[3]);
-            mma_16816(acc, normal2(y0 & lo), normal2(y1 & lo), normal2(y0 & hi), normal2(y1 & hi), q1[0], q1[1], acc[0],
-                      acc[1], acc[2], acc[3]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float s = bf_lo(kp[h][g]), m = bf_hi(kp[h][g]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[k][h][e] = fmaf(s, acc[2 * h + e], fmaf(m, qs[g][e], x[k][h][e]));
-          }
-        }
-      }
-      if (rows < 2 * kC4Rows) {                               // warp-uniform
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (16 * k + 8 * h + r >= rows) {
-              x[k][h][0] = x[k][h][1] = -INFINITY;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) vp[k][h][g] = 0u;
-            }
-      }
-      // ---- softmax against references that move only when a logit passes them by 2^7; the steps' scale likewise
-      float xm[2];
-      uint32_t vmax = 0u;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) xm[e] = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) vmax = max_bf2(vmax, vp[k][h][g]);
-      if (__any_sync(kFullMask, xm[0] > thr[0] || xm[1] > thr[1] || bf_lo(vmax) > s_top)) {
-        // the power of two past the largest step (at least 2^-100, at most 2^126), twice that for room
-        const uint32_t top = __reduce_max_sync(kFullMask, __float_as_uint(bf_lo(vmax)));
-        float beta = 1.0f;
-        if (__uint_as_float(top) > s_top) {
-          const uint32_t e2 = min(max((top >> 23) + 2u, 27u), 253u);
-          const float s_new = __uint_as_float(e2 << 23);
-          beta = s_top / s_new;                               // 0 the first time
-          s_top = s_new;
-          s_mul = __uint_as_float((254u + 7u - e2) << 23);
-        }
-        float al[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = xm[e];
-#pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
-          al[e] = 1.0f;
-          if (mx > thr[e]) {
-            const float mn = mx * c2[e];
-            al[e] = ex2(m_ref[e] - mn);                       // 0 the first time
-            m_ref[e] = mn;
-            thr[e] = (mn + kD4Slack) / c2[e];
-            l_run[e] *= al[e];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) om[g][e] *= al[e];
-          }
-          al[e] *= beta;
-        }
-#pragma unroll
-        for (int t = 0; t < S::MT; ++t) {
-          o[t][0] *= al[0], o[t][1] *= al[1];
-          o[t][2] *= al[0], o[t][3] *= al[1];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[k][h][e] = ex2(fmaf(x[k][h][e], c2[e], -m_ref[e]));   // the weight p
-            l_run[e] += x[k][h][e];
-          }
-
-      // ---- out^T += V^T (p s)
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
-        uint32_t hi[2][2], lo[2][2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float s = bf_lo(vp[k][h][g]), m8 = fmaf(8.0f, s, bf_hi(vp[k][h][g])), sx = s * s_mul;
-            const float p0 = x[k][h][0], p1 = x[k][h][1];
-            om[g][0] = fmaf(p0, m8, om[g][0]);
-            om[g][1] = fmaf(p1, m8, om[g][1]);
-            const float w0 = p0 * sx, w1 = p1 * sx;
-            const uint32_t w = pack_h2(w0, w1);
-            hi[k][h] = transpose8(w);
-            lo[k][h] = transpose8(pack_h2(w0 - h_lo(w), w1 - h_hi(w)));
-          }
-        __syncwarp();
-        uint32_t vw[2][2][2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            lds_words(stage + k * L::BLOCK + L::V_OFF + (4 * t + c) * D + (r * NG + g) * 8, vw[k][t]);
-#pragma unroll
-        for (int wl = 0; wl < 2; ++wl)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {                       // dims 64g + 8r + 4wl + 2h, + 1
-            uint32_t a[2][4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t y0 = vw[k][0][wl], y1 = vw[k][1][wl];
-              if (h == 1) y0 >>= 8, y1 >>= 8;
-              a[k][0] = around0<0>(y0), a[k][1] = around0<4>(y0), a[k][2] = around0<0>(y1), a[k][3] = around0<4>(y1);
-            }
-            float d[4];
-            mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1], 0.0f, 0.0f, 0.0f, 0.0f);
-            mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1], d[0], d[1], d[2], d[3]);
-            mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], hi[0][0], hi[0][1], d[0], d[1], d[2], d[3]);
-            mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], hi[1][0], hi[1][1], d[0], d[1], d[2], d[3]);
-            float(&acc)[4] = o[4 * g + 2 * wl + h];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] += d[j];
-          }
-      }
-      __syncwarp();
-      if (i + kD4Stages < n) {                                // the stage is read: refill it
-        if (((i + kD4Stages) & 31) == 0) look_up(i + kD4Stages);
-        issue(i + kD4Stages, kD4Stages);
-      }
-      ++used;
-    }
-    if (!ok) {                                                // a wait expired: let this warp's own copies land
-      if (lane == 0)
-        for (int i = 0; i < kD4Stages; ++i) mbar_wait_for(&bar[(used + i) % kD4Stages], ((used + i) / kD4Stages) & 1u,
-                                                          20000000ull);
-    }
-
-    // ---- this head's part is read: the warps' states to shared memory
-    const float s_out = s_top * 0x1p2f;                       // 2^E 2^-7 2^9
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) {
-        l_run[e] += __shfl_xor_sync(kFullMask, l_run[e], sh);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) om[g][e] += __shfl_xor_sync(kFullMask, om[g][e], sh);
-      }
-      if (r == 0) {
-        s_m[warp][2 * c + e] = m_ref[e];
-        s_l[warp][2 * c + e] = l_run[e];
-      }
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float* d0 = s_o + (warp * 8 + 2 * c + e) * D + 64 * g + 8 * r;
-#pragma unroll
-        for (int wl = 0; wl < 2; ++wl) {
-          const float(&x0)[4] = o[4 * g + 2 * wl], (&x1)[4] = o[4 * g + 2 * wl + 1];
-          // odd dims' codes were taken 16-fold
-          *reinterpret_cast<float4*>(d0 + 4 * wl) =
-              make_float4(fmaf(x0[e], s_out, om[g][e]), fmaf(x0[2 + e], s_out * 0.0625f, om[g][e]),
-                          fmaf(x1[e], s_out, om[g][e]), fmaf(x1[2 + e], s_out * 0.0625f, om[g][e]));
-        }
-      }
-    }
+    const bool ok = read_part<D>(p, b, count, a0, a1, ring, bar, used, abort_flag, s_o, s_m, s_l);
     const bool failed = __syncthreads_or(!ok);
     if (failed) {                                             // uniform: the output of this share is not written
       if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -554,20 +593,8 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (past ? 1 : 0);
     for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
       const int g = 4 * e4 / D;
-      float M = -INFINITY, Ls = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kD4Warps; ++w) M = fmaxf(M, s_m[w][g]);
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kD4Warps; ++w) {
-        const float mw = s_m[w][g], lw = s_l[w][g];
-        const bool none = mw == -INFINITY && lw == 0.0f;      // the warp had no block
-        const float wgt = none ? 0.0f : exp2f(mw - M);
-        const float4 v = *reinterpret_cast<const float4*>(s_o + w * 8 * D + 4 * e4);
-        Ls = fmaf(lw, wgt, Ls);
-        acc.x = fmaf(v.x, wgt, acc.x), acc.y = fmaf(v.y, wgt, acc.y);
-        acc.z = fmaf(v.z, wgt, acc.z), acc.w = fmaf(v.w, wgt, acc.w);
-      }
+      float M, Ls;
+      const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
       if (whole) {
         reinterpret_cast<float4*>(p.out + b * G * D)[e4] =
             make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
@@ -584,6 +611,76 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     do ++b; while (blocks_of(count_of(b), p.cap) == 0);       // there is a next one: u1 <= total
   }
   if (tid == 0) p.cont[blockIdx.x] = cont;
+}
+
+// Few rows a head: latency counts, and the shares of the other kernel (a scan
+// of all counts, parts of two heads in a CTA, a second launch) cost more than
+// equal work gains.  Here a cluster of CTAs reads a head, rank j the j-th of
+// its equal parts, and joins its CTAs' states through distributed shared
+// memory, each CTA for a part of the dims.
+template <int D>
+__global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4Args p) {
+  using S = D4<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kD4Warps * kD4Stages];
+  __shared__ int s_abort;
+  __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
+  __shared__ float s_cm[8], s_cl[8];                          // this CTA's reference and sum per query
+  __shared__ __align__(16) float s_co[8 * D];                 // and output
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, G = p.G;
+  const int64_t b = blockIdx.x / C;
+  const int count = p.counts[b];                              // the same in all CTAs of the cluster
+  if (count <= 0 || count > p.cap) {
+    if (rank == 0 && count == 0) {
+      for (int e = tid; e < G * D; e += kD4Threads) p.out[b * G * D + e] = 0.0f;
+      if (p.lse2 != nullptr && tid < G) p.lse2[b * G + tid] = -INFINITY;
+    } else if (rank == 0 && tid == 0) {
+      report(p.status, KVZ_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
+  if (tid == 0) s_abort = 0;
+  fence_mbar_init();
+  // parts in whole stages, so that only the head's last block can stand alone
+  const int n_blk = (count + kC4Rows - 1) / kC4Rows, n_st = (n_blk + 1) / 2;
+  const int a0 = 2 * static_cast<int>(static_cast<int64_t>(n_st) * rank / C);
+  const int a1 = min(2 * static_cast<int>(static_cast<int64_t>(n_st) * (rank + 1) / C), n_blk);
+  float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
+  uint32_t used = 0;
+  const bool ok = read_part<D>(p, b, count, a0, a1, smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, used,
+                               &s_abort, s_o, s_m, s_l);
+  const bool failed = __syncthreads_or(!ok);
+  for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
+    const int g = 4 * e4 / D;
+    float M, Ls;
+    const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
+    reinterpret_cast<float4*>(s_co)[e4] = acc;
+    if ((4 * e4) % D == 0) {
+      s_cm[g] = M;
+      s_cl[g] = failed ? NAN : Ls;                            // a part that was not read spoils its head, not others
+    }
+  }
+  cluster.sync();
+  for (int e4 = rank * kD4Threads + tid; e4 < G * D / 4; e4 += C * kD4Threads) {
+    const int g = 4 * e4 / D;
+    float M = -INFINITY, Ls = 0.0f;
+    for (int j = 0; j < C; ++j) M = fmaxf(M, cluster.map_shared_rank(s_cm, j)[g]);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < C; ++j) {
+      const float mj = cluster.map_shared_rank(s_cm, j)[g], lj = cluster.map_shared_rank(s_cl, j)[g];
+      const float wgt = mj == -INFINITY && lj == 0.0f ? 0.0f : exp2f(mj - M);
+      const float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(s_co, j))[e4];
+      Ls = fmaf(lj, wgt, Ls);
+      acc.x = fmaf(v.x, wgt, acc.x), acc.y = fmaf(v.y, wgt, acc.y);
+      acc.z = fmaf(v.z, wgt, acc.z), acc.w = fmaf(v.w, wgt, acc.w);
+    }
+    reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + g] = M + log2f(Ls);
+  }
+  cluster.sync();                                             // the others have read this CTA's state
 }
 
 // The heads that CTA blockIdx.x began and others went on with: their partials
@@ -645,6 +742,25 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
 
 template <int D>
 cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
+  // CTAs per head that fill the GPU once, at most a portable cluster
+  int C = 1;
+  while (C < 8 && 2 * C * a.B <= kD4Workers) C *= 2;
+  if (a.cap <= static_cast<int64_t>(C) * kD4ClusterRows) {
+    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(D4<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(C);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B * C));
+    cfg.blockDim = dim3(kD4Threads);
+    cfg.dynamicSmemBytes = D4<D>::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_int4_cluster_kernel<D>, a);
+  }
   cudaError_t e = smem_limit_once<decode_int4_kernel<D>>(D4<D>::SMEM);
   if (e != cudaSuccess) return e;
   decode_int4_kernel<D><<<kD4Workers, kD4Threads, D4<D>::SMEM, stream>>>(a);
