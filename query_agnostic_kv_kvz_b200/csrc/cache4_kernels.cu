@@ -2,11 +2,8 @@
 // kvz_cache4.cuh): kept rows into it (compaction), new rows behind them with
 // the position rotation on the way (append), and rows back to bf16 (expand).
 //
-// All three move rows through registers, a warp per row pair (d = 128) or two
-// pairs (d = 64), a lane per 8 dims: 16-byte loads and stores on the bf16
-// side; on the 4-bit side a warp's stores of a pair cover its 128 bytes of K
-// codes, 128 of V codes and its scale words whole.  HBM-bound: 4 d bytes of
-// bf16 and 9/8 d bytes of the cache per row.
+// All three move rows through registers.  HBM-bound: 4 d bytes of bf16 and
+// 9/8 d bytes of the cache per row.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -22,144 +19,316 @@ namespace kvz {
 namespace {
 
 constexpr int kC4Threads = 256;
-constexpr int kC4Unroll = 4;                                  // units of a warp in flight
+#ifndef KVZ_C4_CC
+#define KVZ_C4_CC 2
+#endif
+#ifndef KVZ_C4_EC
+#define KVZ_C4_EC 3
+#endif
+constexpr int kCompactCtas = KVZ_C4_CC;                       // CTAs per SM, all resident at once
+constexpr int kExpandCtas = KVZ_C4_EC;
 
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (N == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
 }
 
-// The pairs of all heads as one index space: head b's pairs start at
-// pair_base(b) = offsets[b] / 2 + b, which leaves room for one more than half
-// its rows (a run of n rows touches at most n / 2 + 1 pairs), so a unit finds
-// its head by bisection and heads of any lengths share the grid evenly.
-__device__ __forceinline__ int64_t pair_base(const int64_t* offsets, int64_t b) { return (offsets[b] >> 1) + b; }
-__device__ __forceinline__ int64_t head_of(const int64_t* offsets, int64_t B, int64_t u) {
-  int64_t lo = 0, hi = B - 1;                                 // largest b with pair_base(b) <= u
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (pair_base(offsets, mid) <= u) lo = mid; else hi = mid - 1;
+// The blocks of all heads as one index space: head b's start at
+// block_base(b) = offsets[b] / 16 + SPARE * b, so heads of any lengths share
+// the grid evenly: a warp takes an equal run of blocks, finds the first one's
+// head by bisection and walks on from there.  A head of n rows has at most
+// n / 16 + 1 blocks from its row 0 on (SPARE = 1), and a run of n rows that
+// begins inside one touches at most n / 16 + 2 (SPARE = 2).
+template <int SPARE>
+struct BlockWalk {
+  int64_t u, end;                                             // this warp's run of units
+  int64_t b, base, next, o;                                   // head, its first unit, the next head's, offsets[b]
+  int32_t n, f;                                               // rows [f, n) of the head count (none for a bad head)
+
+  static __device__ __forceinline__ int64_t block_base(const int64_t* offsets, int64_t b) {
+    return (offsets[b] >> 4) + SPARE * b;
   }
-  return lo;
+  __device__ __forceinline__ void run(const int64_t* offsets, int64_t B) {
+    const int64_t total = block_base(offsets, B);
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
+    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / 32);
+    const int64_t each = (total + n_warps - 1) / n_warps;
+    u = warp * each;
+    end = u + each < total ? u + each : total;
+  }
+  __device__ __forceinline__ int64_t head(const int64_t* offsets, int64_t B) const {
+    int64_t lo = 0, hi = B - 1;                               // largest b with block_base(b) <= u
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (block_base(offsets, mid) <= u) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// Both kernels below take a block of 16 rows per warp: lane (r, c) = (lane / 4,
+// lane % 4) holds dims 64g + 16c .. 64g + 16c + 15 of rows r and r + 8, which
+// are its words of the K layout.  All index arithmetic is per block; the
+// block's codes move as one 16-byte access per lane and tensor half.
+
+// A row's V halves meet their pair's other row's here: lanes 4 apart hold rows
+// r and r ^ 1.  vv[g][j]: the lane's own units of r' = 2c + j (two halves of a
+// word); after the exchange an even row's lane holds both rows' words of r' =
+// 2c, an odd row's those of 2c + 1: words [g][w].
+template <int NG>
+__device__ __forceinline__ void pair_up(const uint32_t (&vv)[NG][2], bool odd, uint32_t (&out)[2 * NG]) {
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const uint32_t mine = odd ? vv[g][1] : vv[g][0];
+    const uint32_t got = __shfl_xor_sync(kFullMask, odd ? vv[g][0] : vv[g][1], 4);
+    const uint32_t even_row = odd ? got : mine, odd_row = odd ? mine : got;
+    out[2 * g] = __byte_perm(even_row, odd_row, 0x5410);
+    out[2 * g + 1] = __byte_perm(even_row, odd_row, 0x7632);
+  }
+}
+template <int NG>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[2 * NG]) {
+  if constexpr (NG == 2) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kC4Threads)
+__global__ void __launch_bounds__(kC4Threads, 2)
     compact_int4_kernel(const uint16_t* __restrict__ K, const uint16_t* __restrict__ V, int64_t B, int64_t n_c,
                         const int32_t* __restrict__ idx, const int32_t* __restrict__ counts,
                         const int64_t* __restrict__ offsets, Pages4 pg, int64_t cap, int32_t* status) {
   using L = C4<D>;
-  constexpr int PW = 16 / L::LPR;                             // pairs per warp step: 1 or 2
-  const int lane = threadIdx.x & 31, l = lane % L::LPR;
-  const int e = (lane / L::LPR) & 1, sub = lane / (2 * L::LPR);
-  const int64_t total = pair_base(offsets, B);
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
-  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / 32);
-  for (int64_t u0 = warp * (PW * kC4Unroll); u0 < total; u0 += n_warps * (PW * kC4Unroll)) {
-    int64_t b = head_of(offsets, B, u0);
-    uint4 kv[kC4Unroll], vv[kC4Unroll];
-    uint8_t* blk[kC4Unroll];
-    int row[kC4Unroll];
-#pragma unroll
-    for (int i = 0; i < kC4Unroll; ++i) {
-      const int64_t u = u0 + i * PW + sub;
-      blk[i] = nullptr;
-      row[i] = e;
-      kv[i] = vv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (u >= total) continue;
-      while (b + 1 < B && pair_base(offsets, b + 1) <= u) ++b;
-      const int64_t n = counts[b], o = offsets[b];
-      const int64_t p = 2 * (u - pair_base(offsets, b)) + e;  // slot of this lane's row
-      if (n < 0 || n > offsets[b + 1] - o || n > cap) {
-        if (p == 0 && l == 0) report(status, KVZ_ERR_INVALID_ARG);
-        continue;
-      }
-      if (p >= n) continue;
-      blk[i] = block_at<D>(pg, b, static_cast<uint32_t>(p >> 4), status);
-      row[i] = static_cast<int>(p & 15);
-      const int64_t j = idx[o + p];
-      if (j >= 0 && j < n_c) {
-        const int64_t at = (b * n_c + j) * D + 8 * l;
-        kv[i] = ld_stream16(K + at);
-        vv[i] = ld_stream16(V + at);
-      } else if (l == 0) {
-        report(status, KVZ_ERR_INVALID_ARG);                  // idx out of [0, n_c): a row of zeros
-      }
+  constexpr int NG = L::NG;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  BlockWalk<1> h;
+  h.run(offsets, B);
+  if (h.u >= h.end) return;                                   // warp-uniform, as is all that follows per block
+  auto enter = [&](int64_t b) {
+    h.b = b;
+    h.o = offsets[b];
+    const int64_t o1 = offsets[b + 1];
+    h.base = (h.o >> 4) + b;
+    h.next = (o1 >> 4) + b + 1;
+    h.n = counts[b];
+    if (h.n < 0 || h.n > o1 - h.o || h.n > cap) {
+      if (lane == 0) report(status, KVZ_ERR_INVALID_ARG);
+      h.n = 0;
     }
+  };
+  enter(h.head(offsets, B));
+  // where a block goes and its rows come from, looked up a step before they move
+  uint8_t* blk = nullptr;
+  int rows = 0;                                               // rows of it that count
+  int64_t src[2];                                             // element of row r + 8h's first dims here; < 0: zeros
+  auto look_up = [&](int64_t u) {
+    blk = nullptr;
+    if (u >= h.end) return;
+    while (u >= h.next && h.b + 1 < B) enter(h.b + 1);
+    const int64_t p0 = (u - h.base) * kC4Rows;
+    if (p0 >= h.n) return;
+    blk = block_at<D>(pg, h.b, static_cast<uint32_t>(u - h.base), status);
+    rows = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);
 #pragma unroll
-    for (int i = 0; i < kC4Unroll; ++i) {
-      uint32_t code[8], sm;
-      bool fine = quantise8(kv[i], code, sm);
-      if (blk[i] != nullptr) store_k<D>(blk[i], row[i], l, code, fine, sm);
-      fine = quantise8(vv[i], code, sm);
-      store_v<D>(blk[i], row[i], l, code, fine, sm, blk[i] != nullptr);
+    for (int k = 0; k < 2; ++k) {
+      src[k] = -1;
+      if (r + 8 * k >= rows) continue;
+      const int64_t j = idx[h.o + p0 + r + 8 * k];
+      if (j >= 0 && j < n_c) src[k] = (h.b * n_c + j) * D + 16 * c;
+      else if (c == 0) report(status, KVZ_ERR_INVALID_ARG);   // idx out of [0, n_c): a row of zeros
     }
+  };
+  look_up(h.u);
+  for (; h.u < h.end; ++h.u) {
+    uint8_t* const to = blk;
+    const int live = rows;
+    uint4 x[2][2][NG][2];                                     // [K, V][row r + 8k][g][half]
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool on = to != nullptr && r + 8 * k < live && src[k] >= 0;
+          x[0][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(K + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
+          x[1][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(V + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
+        }
+    look_up(h.u + 1);
+    if (to == nullptr) continue;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = r + 8 * k;
+        const bool on = row < live;
+        uint32_t kw[2 * NG], vv[NG][2], sm = 0u;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint4 (&v)[2] = x[t][k][g];
+          const Scale4 q = group_scale<4>(
+              min_nan2(min_nan2(min_nan2(v[0].x, v[0].y), min_nan2(v[0].z, v[0].w)),
+                       min_nan2(min_nan2(v[1].x, v[1].y), min_nan2(v[1].z, v[1].w))),
+              max_nan2(max_nan2(max_nan2(v[0].x, v[0].y), max_nan2(v[0].z, v[0].w)),
+                       max_nan2(max_nan2(v[1].x, v[1].y), max_nan2(v[1].z, v[1].w))));
+          if (c == g) sm = q.word;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t code[8];
+            code2(v[j].x, q, code[0], code[1]);
+            code2(v[j].y, q, code[2], code[3]);
+            code2(v[j].z, q, code[4], code[5]);
+            code2(v[j].w, q, code[6], code[7]);
+            if (t == 0) kw[2 * g + j] = k_word(code, q.fine);
+            else vv[g][j] = v_units(code, q.fine);
+          }
+        }
+        if (on && c < NG)
+          *reinterpret_cast<uint32_t*>(to + (t == 0 ? L::KS_OFF : L::VS_OFF) + (row * NG + c) * 4) = sm;
+        if (t == 0) {
+          if (on) store_words<NG>(to + row * (D / 2) + c * (8 * NG), kw);
+          continue;
+        }
+        const bool odd = (row & 1) != 0;
+        uint8_t* const pair = to + L::V_OFF + (row >> 1) * D;
+        uint32_t both[2 * NG];
+        pair_up<NG>(vv, odd, both);
+        if ((row | 1) < live) {
+          store_words<NG>(pair + (2 * c + (odd ? 1 : 0)) * (8 * NG), both);
+        } else if (on) {                                      // the last row of an odd count: its halves alone
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint16_t* const at = reinterpret_cast<uint16_t*>(pair + (2 * c + j) * (8 * NG) + g * 8);
+              at[0] = static_cast<uint16_t>(vv[g][j]);
+              at[2] = static_cast<uint16_t>(vv[g][j] >> 16);
+            }
+        }
+      }
   }
 }
 
 // Rows first[b] .. counts[b] - 1 as bf16 rows offsets[b], offsets[b] + 1, ...
+// A value is one fused bf16 multiply-add, s * code + m rounded once.
 template <int D>
 __global__ void __launch_bounds__(kC4Threads)
     expand_int4_kernel(Pages4 pg, const int32_t* __restrict__ counts, const int32_t* __restrict__ first,
                        const int64_t* __restrict__ offsets, int64_t B, int64_t cap, uint16_t* __restrict__ K_out,
                        uint16_t* __restrict__ V_out, int64_t n_rows, int32_t* status) {
   using L = C4<D>;
-  constexpr int PW = 16 / L::LPR;
-  const int lane = threadIdx.x & 31, l = lane % L::LPR;
-  const int e = (lane / L::LPR) & 1, sub = lane / (2 * L::LPR);
-  const int g = l / 8, c = (l % 8) / 2, uu = l % 2, r = l % 8;
-  const int64_t total = pair_base(offsets, B);
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
-  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / 32);
-  for (int64_t u0 = warp * (PW * kC4Unroll); u0 < total; u0 += n_warps * (PW * kC4Unroll)) {
-    int64_t b = head_of(offsets, B, u0);
-    uint32_t kw[kC4Unroll], ks[kC4Unroll], vs[kC4Unroll];
-    uint2 vw[kC4Unroll];
-    int64_t dst[kC4Unroll];
-#pragma unroll
-    for (int i = 0; i < kC4Unroll; ++i) {
-      const int64_t u = u0 + i * PW + sub;
-      dst[i] = -1;
-      if (u >= total) continue;
-      while (b + 1 < B && pair_base(offsets, b + 1) <= u) ++b;
-      const int64_t n = counts[b], f = first == nullptr ? 0 : first[b], o = offsets[b];
-      const int64_t p = 2 * ((f >> 1) + u - pair_base(offsets, b)) + e;
-      if (f < 0 || n < f || n > cap || n - f > offsets[b + 1] - o || o < 0 || o + (n - f) > n_rows) {
-        if (u == pair_base(offsets, b) && l == 0) report(status, KVZ_ERR_INVALID_ARG);
-        continue;
-      }
-      if (p < f || p >= n) continue;
-      const uint8_t* blk = block_at<D>(pg, b, static_cast<uint32_t>(p >> 4), status);
-      if (blk == nullptr) continue;
-      const int row = static_cast<int>(p & 15);
-      kw[i] = __ldg(reinterpret_cast<const uint32_t*>(blk + row * (D / 2) + (c * L::NG * 2 + g * 2 + uu) * 4));
-      vw[i] = __ldg(reinterpret_cast<const uint2*>(blk + L::V_OFF + (row >> 1) * D + (r * L::NG + g) * 8));
-      ks[i] = __ldg(reinterpret_cast<const uint32_t*>(blk + L::KS_OFF + (row * L::NG + g) * 4));
-      vs[i] = __ldg(reinterpret_cast<const uint32_t*>(blk + L::VS_OFF + (row * L::NG + g) * 4));
-      dst[i] = (o + p - f) * D + 8 * l;
+  constexpr int NG = L::NG;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  BlockWalk<2> h;
+  h.run(offsets, B);
+  if (h.u >= h.end) return;
+  auto enter = [&](int64_t b) {
+    h.b = b;
+    h.o = offsets[b];
+    const int64_t o1 = offsets[b + 1];
+    h.base = (h.o >> 4) + 2 * b;
+    h.next = (o1 >> 4) + 2 * b + 2;
+    h.n = counts[b];
+    h.f = first == nullptr ? 0 : first[b];
+    if (h.f < 0 || h.n < h.f || h.n > cap || h.n - h.f > o1 - h.o || h.o < 0 || h.o + (h.n - h.f) > n_rows) {
+      if (lane == 0) report(status, KVZ_ERR_INVALID_ARG);
+      h.n = h.f = 0;
     }
+  };
+  enter(h.head(offsets, B));
+  const uint8_t* blk = nullptr;
+  int from = 0, to = 0;                                       // rows of the block that count
+  int64_t dst = 0;                                            // output row of the block's row 0
+  auto look_up = [&](int64_t u) {
+    blk = nullptr;
+    if (u >= h.end) return;
+    while (u >= h.next && h.b + 1 < B) enter(h.b + 1);
+    const int64_t q = (h.f >> 4) + u - h.base, p0 = q * kC4Rows;
+    if (p0 >= h.n) return;
+    blk = block_at<D>(pg, h.b, static_cast<uint32_t>(q), status);
+    from = static_cast<int>(h.f > p0 ? h.f - p0 : 0);
+    to = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);
+    dst = h.o + p0 - h.f;
+  };
+  // 32 bytes of a row, as one store where the outputs allow it
+  const bool wide = ((reinterpret_cast<uintptr_t>(K_out) | reinterpret_cast<uintptr_t>(V_out)) & 31u) == 0;
+  auto put32 = [&](uint16_t* at, const uint32_t (&w)[8]) {
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    } else {
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  };
+  look_up(h.u);
+  for (; h.u < h.end; ++h.u) {
+    const uint8_t* const p = blk;
+    const int lo = from, hi = to;
+    const int64_t out = dst;
+    uint32_t kw[2][2 * NG], ks[2][NG], vw[2][2 * NG], vs[2][2 * NG];
+    if (p != nullptr) {
 #pragma unroll
-    for (int i = 0; i < kC4Unroll; ++i) {
-      if (dst[i] < 0) continue;
-      float s = bf_lo(ks[i]), m = bf_hi(ks[i]);
-      const uint32_t w = __funnelshift_r(kw[i], kw[i], 3);
-      uint4 y;
-      y.x = pack_bf2(widen4(w, s, m), widen4(w >> 16, s, m));
-      y.y = pack_bf2(widen4(w >> 4, s, m), widen4(w >> 20, s, m));
-      y.z = pack_bf2(widen4(w >> 8, s, m), widen4(w >> 24, s, m));
-      y.w = pack_bf2(widen4(w >> 12, s, m), widen4(w >> 28, s, m));
-      *reinterpret_cast<uint4*>(K_out + dst[i]) = y;
-      s = bf_lo(vs[i]), m = bf_hi(vs[i]);
-      const uint32_t h = e ? 16u : 0u;
-      const uint32_t a = vw[i].x >> h, z = vw[i].y >> h;
-      y.x = pack_bf2(widen4(a, s, m), widen4(a >> 4, s, m));
-      y.y = pack_bf2(widen4(a >> 8, s, m), widen4(a >> 12, s, m));
-      y.z = pack_bf2(widen4(z, s, m), widen4(z >> 4, s, m));
-      y.w = pack_bf2(widen4(z >> 8, s, m), widen4(z >> 12, s, m));
-      *reinterpret_cast<uint4*>(V_out + dst[i]) = y;
+      for (int k = 0; k < 2; ++k) {
+        load_words<2 * NG>(p + (r + 8 * k) * (D / 2) + c * (8 * NG), kw[k]);
+        load_words<NG>(p + L::KS_OFF + (r + 8 * k) * (4 * NG), ks[k]);
+        // V: lane (r, c) takes r' = r of the pairs c and c + 4, rows 2c + 8k and 2c + 8k + 1
+        load_words<2 * NG>(p + L::V_OFF + (c + 4 * k) * D + r * (8 * NG), vw[k]);
+        load_words<2 * NG>(p + L::VS_OFF + (2 * c + 8 * k) * (4 * NG), vs[k]);
+      }
+    }
+    look_up(h.u + 1);
+    if (p == nullptr) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = r + 8 * k;
+      if (row >= lo && row < hi) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t s2 = __byte_perm(ks[k][g], 0u, 0x1010), m2 = __byte_perm(ks[k][g], 0u, 0x3232);
+          uint32_t y[8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t w = kw[k][2 * g + u];
+            y[4 * u] = fma_bf2(s2, code_bf2(w), m2);
+            y[4 * u + 1] = fma_bf2(s2, code_bf2(w >> 4), m2);
+            y[4 * u + 2] = fma_bf2(s2, code_bf2(w >> 8), m2);
+            y[4 * u + 3] = fma_bf2(s2, code_bf2(__funnelshift_r(w, w, 12)), m2);
+          }
+          put32(K_out + (out + row) * D + 64 * g + 16 * c, y);
+        }
+      }
+      const int even = 2 * c + 8 * k;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        // (even row, odd row) in the halves of every word
+        const uint32_t s2 = __byte_perm(vs[k][g], vs[k][NG + g], 0x5410);
+        const uint32_t m2 = __byte_perm(vs[k][g], vs[k][NG + g], 0x7632);
+        uint32_t z[8];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t v = vw[k][2 * g + w];
+          z[4 * w] = fma_bf2(s2, code_bf2(v << 3), m2);
+          z[4 * w + 1] = fma_bf2(s2, code_bf2(v >> 1), m2);
+          z[4 * w + 2] = fma_bf2(s2, code_bf2(v >> 5), m2);
+          z[4 * w + 3] = fma_bf2(s2, code_bf2(v >> 9), m2);
+        }
+        uint16_t* const at = V_out + (out + even) * D + 64 * g + 8 * r;
+        if (even >= lo && even < hi)
+          *reinterpret_cast<uint4*>(at) = make_uint4(__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410),
+                                                     __byte_perm(z[4], z[5], 0x5410), __byte_perm(z[6], z[7], 0x5410));
+        if (even + 1 >= lo && even + 1 < hi)
+          *reinterpret_cast<uint4*>(at + D) =
+              make_uint4(__byte_perm(z[0], z[1], 0x7632), __byte_perm(z[2], z[3], 0x7632),
+                         __byte_perm(z[4], z[5], 0x7632), __byte_perm(z[6], z[7], 0x7632));
+      }
     }
   }
 }
@@ -309,10 +478,10 @@ cudaError_t launch_compact_int4(const void* K, const void* V, int64_t B, int64_t
                                 cudaStream_t stream) {
   const uint16_t *k = static_cast<const uint16_t*>(K), *v = static_cast<const uint16_t*>(V);
   if (d == 128)
-    compact_int4_kernel<128><<<persistent_grid(4), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
+    compact_int4_kernel<128><<<persistent_grid(kCompactCtas), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
                                                                             table_rows(pg), status);
   else
-    compact_int4_kernel<64><<<persistent_grid(4), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
+    compact_int4_kernel<64><<<persistent_grid(kCompactCtas), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
                                                                            table_rows(pg), status);
   return cudaGetLastError();
 }
@@ -322,10 +491,10 @@ cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const in
                                cudaStream_t stream) {
   uint16_t *k = static_cast<uint16_t*>(K_out), *v = static_cast<uint16_t*>(V_out);
   if (d == 128)
-    expand_int4_kernel<128><<<persistent_grid(4), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
+    expand_int4_kernel<128><<<persistent_grid(kExpandCtas), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
                                                                            table_rows(pg), k, v, n_rows, status);
   else
-    expand_int4_kernel<64><<<persistent_grid(4), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
+    expand_int4_kernel<64><<<persistent_grid(kExpandCtas), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
                                                                           table_rows(pg), k, v, n_rows, status);
   return cudaGetLastError();
 }

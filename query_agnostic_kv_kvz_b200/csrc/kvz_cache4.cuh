@@ -52,8 +52,21 @@ __device__ __forceinline__ uint8_t* block_at(const Pages4& pg, int64_t b, uint32
   return pg.cache + (static_cast<int64_t>(id) * pg.blocks + (blk - pi * pg.blocks)) * C4<D>::BLOCK;
 }
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// x (the low or high bf16 of w) + y, rounded once: one full-rate instruction,
+// where a shift or mask to widen x first would take two issues of the
+// half-rate integer pipe.
+__device__ __forceinline__ float add_lo(uint32_t w, float y) {
+  float d;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.rn.f32.bf16 %0, l, %2;}" : "=f"(d) : "r"(w), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float add_hi(uint32_t w, float y) {
+  float d;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.rn.f32.bf16 %0, h, %2;}" : "=f"(d) : "r"(w), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return add_lo(w, 0.0f); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return add_hi(w, 0.0f); }
 
 __device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -71,41 +84,73 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return r;
 }
 
-// Codes and scale word of the 8 consecutive values in x; the group of 64 is
-// the 8 lanes that differ in the low three bits (all lanes take part).  With
-// m = min, r = max - min: step s = bf16(r * (1/15)), code = round((x - m) *
-// (1/s)), every step one IEEE float32 operation, ties to even.  (r * (1/15)
-// rounded to bf16 is at least r/15 * (1 - 2^-8), so a code is at most 15.06
-// before it is rounded.)  A step below 2^-126 is held as 0, with codes 0: its
-// reciprocal leaves float32, and the whole group is within 2^-122 of m.  A
-// group whose range is not finite (a NaN, an infinity or a range past
-// float32) is held as step NaN, so reading it gives NaN.
-// code[i] = 0x4B400000 + the code of value i.
-__device__ __forceinline__ bool quantise8(const uint4& x, uint32_t (&code)[8], uint32_t& sm) {
-  const uint32_t lo2 = min_nan2(min_nan2(x.x, x.y), min_nan2(x.z, x.w));
-  const uint32_t hi2 = max_nan2(max_nan2(x.x, x.y), max_nan2(x.z, x.w));
+// Quantisation of a row's group of 64 values, held by LANES lanes that differ
+// in the low bits of the lane number (all lanes of the warp take part).  With m = min, r = max - min: step
+// s = bf16(r * (1/15)), code = round((x - m) * (1/s)), every step one IEEE
+// float32 operation, ties to even.  (r * (1/15) rounded to bf16 is at least
+// r/15 * (1 - 2^-8), so a code is at most 15.06 before it is rounded.)  A step
+// below 2^-126 is held as 0, with codes 0: its reciprocal leaves float32, and
+// the whole group is within 2^-122 of m.  A group whose range is not finite (a
+// NaN, an infinity or a range past float32) is held as step NaN, so reading it
+// gives NaN.
+struct Scale4 {
+  float m, inv;
+  uint32_t word;                                              // bf16 s, bf16 m
+  bool fine;
+};
+// lo2, hi2: minima and maxima of the lane's own values, over even and odd ones.
+template <int LANES>
+__device__ __forceinline__ Scale4 group_scale(uint32_t lo2, uint32_t hi2) {
   // (min, -max) in one word, so that one minimum over the lanes serves both
   uint32_t v = __byte_perm(min_nan2(lo2, lo2 >> 16), max_nan2(hi2, hi2 >> 16) ^ 0x8000u, 0x5410);
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) v = min_nan2(v, __shfl_xor_sync(kFullMask, v, o));
-  const float m = bf_lo(v), r = __fadd_rn(__uint_as_float((v ^ 0x80000000u) & 0xFFFF0000u), -m);
-  const bool fine = r < INFINITY;
+  for (int o = 1; o < LANES; o <<= 1) v = min_nan2(v, __shfl_xor_sync(kFullMask, v, o));
+  Scale4 q;
+  q.m = bf_lo(v);
+  const float r = add_hi(v ^ 0x80000000u, -q.m);
+  q.fine = r < INFINITY;
   float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(r, 1.0f / 15.0f)));
   s = s < 0x1p-126f ? 0.0f : s;
-  const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-  sm = fine ? ((__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u)) : 0x00007FC0u;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    code[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(bf_lo(w[i]), m), inv), 12582912.0f));
-    code[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(bf_hi(w[i]), m), inv), 12582912.0f));
-  }
-  return fine;
+  q.inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  q.word = q.fine ? ((__float_as_uint(s) >> 16) | (v << 16)) : 0x00007FC0u;
+  return q;
+}
+// 0x4B400000 + the codes of the two values in w.
+__device__ __forceinline__ void code2(uint32_t w, const Scale4& q, uint32_t& c0, uint32_t& c1) {
+  c0 = __float_as_uint(__fadd_rn(__fmul_rn(add_lo(w, -q.m), q.inv), 12582912.0f));
+  c1 = __float_as_uint(__fadd_rn(__fmul_rn(add_hi(w, -q.m), q.inv), 12582912.0f));
+}
+// Scale and codes (+ 0x4B400000) of a group that 8 lanes hold, 8 values each.
+__device__ __forceinline__ bool quantise8(const uint4& x, uint32_t (&code)[8], uint32_t& sm) {
+  const Scale4 q = group_scale<8>(min_nan2(min_nan2(x.x, x.y), min_nan2(x.z, x.w)),
+                                  max_nan2(max_nan2(x.x, x.y), max_nan2(x.z, x.w)));
+  code2(x.x, q, code[0], code[1]);
+  code2(x.y, q, code[2], code[3]);
+  code2(x.z, q, code[4], code[5]);
+  code2(x.w, q, code[6], code[7]);
+  sm = q.word;
+  return q.fine;
 }
 
 // Sum of code[i] << shift with the constant 0x4B400000 parts taken out (the
 // arithmetic is modulo 2^32, so they cancel exactly).
 constexpr uint32_t kCodeBias = 0x4B400000u;
+
+// A K word: 8 codes as nibbles 0, 2, 4, 6, 1, 3, 5, 7, rotated left by 3.
+__device__ __forceinline__ uint32_t k_word(const uint32_t (&code)[8], bool fine) {
+  constexpr uint32_t bias = kCodeBias * 0x11111111u;
+  uint32_t w = code[0] + (code[1] << 16) + (code[2] << 4) + (code[3] << 20) + (code[4] << 8) + (code[5] << 24) +
+               (code[6] << 12) + (code[7] << 28) - bias;
+  w = fine ? w : 0u;
+  return __funnelshift_l(w, w, 3);
+}
+// Two V units of one row: codes 0..3 in the low half, 4..7 in the high half.
+__device__ __forceinline__ uint32_t v_units(const uint32_t (&code)[8], bool fine) {
+  constexpr uint32_t bias = kCodeBias * 0x1111u;
+  const uint32_t u0 = code[0] + (code[1] << 4) + (code[2] << 8) + (code[3] << 12) - bias;
+  const uint32_t u1 = code[4] + (code[5] << 4) + (code[6] << 8) + (code[7] << 12) - bias;
+  return fine ? __byte_perm(u0, u1, 0x5410) : 0u;
+}
 
 // Write one row pair's K codes: lane l of the row's D / 8 lanes holds dims
 // 8l .. 8l + 7, which are one word of the row.
@@ -113,11 +158,7 @@ template <int D>
 __device__ __forceinline__ void store_k(uint8_t* blk, int row, int l, const uint32_t (&code)[8], bool fine,
                                         uint32_t sm) {
   using L = C4<D>;
-  constexpr uint32_t bias = kCodeBias * 0x11111111u;
-  uint32_t w = code[0] + (code[1] << 16) + (code[2] << 4) + (code[3] << 20) + (code[4] << 8) + (code[5] << 24) +
-               (code[6] << 12) + (code[7] << 28) - bias;
-  w = fine ? w : 0u;
-  w = __funnelshift_l(w, w, 3);
+  const uint32_t w = k_word(code, fine);
   const int g = l / 8, c = (l % 8) / 2, u = l % 2;
   *reinterpret_cast<uint32_t*>(blk + row * (D / 2) + (c * L::NG * 2 + g * 2 + u) * 4) = w;
   if (l % 8 == 0) *reinterpret_cast<uint32_t*>(blk + L::KS_OFF + (row * L::NG + g) * 4) = sm;
@@ -130,11 +171,7 @@ template <int D>
 __device__ __forceinline__ void store_v(uint8_t* blk, int row, int l, const uint32_t (&code)[8], bool fine,
                                         uint32_t sm, bool write) {
   using L = C4<D>;
-  constexpr uint32_t bias = kCodeBias * 0x1111u;
-  uint32_t h0 = (code[0] + (code[1] << 4) + (code[2] << 8) + (code[3] << 12) - bias) & 0xFFFFu;
-  uint32_t h1 = (code[4] + (code[5] << 4) + (code[6] << 8) + (code[7] << 12) - bias) & 0xFFFFu;
-  h0 = fine ? h0 : 0u;
-  h1 = fine ? h1 : 0u;
+  const uint32_t vu = v_units(code, fine), h0 = vu & 0xFFFFu, h1 = vu >> 16;
   const bool odd = (row & 1) != 0;
   const uint32_t got = __shfl_xor_sync(kFullMask, (odd ? h0 : h1) | (write ? 0x10000u : 0u), L::LPR);
   const bool both = write && (got & 0x10000u) != 0;
@@ -150,10 +187,16 @@ __device__ __forceinline__ void store_v(uint8_t* blk, int row, int l, const uint
   if (write && l % 8 == 0) *reinterpret_cast<uint32_t*>(blk + L::VS_OFF + (row * L::NG + g) * 4) = sm;
 }
 
-// s * code + m of the code in the low four bits of w (one rounding: s * code
-// is exact in float32).
-__device__ __forceinline__ float widen4(uint32_t w, float s, float m) {
-  return __fmaf_rn(s, __uint_as_float((w & 15u) | 0x4B000000u) - 8388608.0f, m);
+// Two codes, one in each half of w with its four bits from bit 3 up, as bf16.
+__device__ __forceinline__ uint32_t code_bf2(uint32_t w) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((w & 0x00780078u) | 0x41804180u), "r"(0xC180C180u));   // 16 + code - 16
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_bf2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
 }  // namespace kvz
