@@ -19,14 +19,8 @@ namespace kvz {
 namespace {
 
 constexpr int kC4Threads = 256;
-#ifndef KVZ_C4_CC
-#define KVZ_C4_CC 2
-#endif
-#ifndef KVZ_C4_EC
-#define KVZ_C4_EC 3
-#endif
-constexpr int kCompactCtas = KVZ_C4_CC;                       // CTAs per SM, all resident at once
-constexpr int kExpandCtas = KVZ_C4_EC;
+constexpr int kCompactCtas = 2;                               // CTAs per SM of the largest grids: resident at once, and
+constexpr int kExpandCtas = 12;                               // four waves (measured: 2, 4, 6 and 3, 4, 8, 12, 24)
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -467,7 +461,11 @@ __global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, 
   }
 }
 
-unsigned persistent_grid(int per_sm) { return 148u * static_cast<unsigned>(per_sm); }
+// CTAs for `units` warp units: one each, up to per_sm on every SM, over which the units are then shared out evenly.
+unsigned grid_for(int64_t units, int per_sm) {
+  const int64_t n = (units + kC4Threads / 32 - 1) / (kC4Threads / 32), top = int64_t(148) * per_sm;
+  return static_cast<unsigned>(n < 1 ? 1 : (n < top ? n : top));
+}
 
 int64_t table_rows(const Pages4& pg) { return pg.max_pages * pg.blocks * kC4Rows; }
 
@@ -477,11 +475,12 @@ cudaError_t launch_compact_int4(const void* K, const void* V, int64_t B, int64_t
                                 const int32_t* counts, const int64_t* offsets, const Pages4& pg, int32_t* status,
                                 cudaStream_t stream) {
   const uint16_t *k = static_cast<const uint16_t*>(K), *v = static_cast<const uint16_t*>(V);
+  const unsigned grid = grid_for(B * (table_rows(pg) / kC4Rows + 1), kCompactCtas);   // (the counts are on the device)
   if (d == 128)
-    compact_int4_kernel<128><<<persistent_grid(kCompactCtas), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
+    compact_int4_kernel<128><<<grid, kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
                                                                             table_rows(pg), status);
   else
-    compact_int4_kernel<64><<<persistent_grid(kCompactCtas), kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
+    compact_int4_kernel<64><<<grid, kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
                                                                            table_rows(pg), status);
   return cudaGetLastError();
 }
@@ -490,11 +489,12 @@ cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const in
                                int64_t B, int d, void* K_out, void* V_out, int64_t n_rows, int32_t* status,
                                cudaStream_t stream) {
   uint16_t *k = static_cast<uint16_t*>(K_out), *v = static_cast<uint16_t*>(V_out);
+  const unsigned grid = grid_for(n_rows / kC4Rows + 2 * B, kExpandCtas);
   if (d == 128)
-    expand_int4_kernel<128><<<persistent_grid(kExpandCtas), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
+    expand_int4_kernel<128><<<grid, kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
                                                                            table_rows(pg), k, v, n_rows, status);
   else
-    expand_int4_kernel<64><<<persistent_grid(kExpandCtas), kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
+    expand_int4_kernel<64><<<grid, kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
                                                                           table_rows(pg), k, v, n_rows, status);
   return cudaGetLastError();
 }

@@ -98,6 +98,14 @@ struct Scale4 {
   uint32_t word;                                              // bf16 s, bf16 m
   bool fine;
 };
+// 1 / s for a positive normal bf16 s up to 2^125, correctly rounded: the
+// approximate reciprocal and one Newton step, which agrees with division for
+// every one of those 32,128 values, in 3 instructions without a slow path.
+__device__ __forceinline__ float step_inverse(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return __fmaf_rn(y, __fmaf_rn(-s, y, 1.0f), y);
+}
 // lo2, hi2: minima and maxima of the lane's own values, over even and odd ones.
 template <int LANES>
 __device__ __forceinline__ Scale4 group_scale(uint32_t lo2, uint32_t hi2) {
@@ -111,7 +119,7 @@ __device__ __forceinline__ Scale4 group_scale(uint32_t lo2, uint32_t hi2) {
   q.fine = r < INFINITY;
   float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(r, 1.0f / 15.0f)));
   s = s < 0x1p-126f ? 0.0f : s;
-  q.inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  q.inv = s > 0.0f ? step_inverse(s) : 0.0f;
   q.word = q.fine ? ((__float_as_uint(s) >> 16) | (v << 16)) : 0x00007FC0u;
   return q;
 }
