@@ -470,8 +470,9 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /* kvz_decode_int4: kvz_decode over the 4-bit cache: q [B][G][d] bf16, out   */
 /*   [B][G][d] fp32, lse2 [B][G] fp32 (optional); a head without rows gives  */
 /*   out = 0, lse2 = -inf.  1 <= G <= 8.  Workspace:                         */
-/*   kvz_decode_int4_workspace_size(G, d) bytes, 256-byte aligned; it needs  */
-/*   no initial value and is free again when the call has finished.          */
+/*   kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d) bytes    */
+/*   (0 where heads are short: NULL then), 256-byte aligned; it needs no     */
+/*   initial value and is free again when the call has finished.             */
 /*                                                                          */
 /* Device-detected errors (KVZ_ERR_INVALID_ARG in d_status): a count outside */
 /* [0, max_pages * page_size] (the head is left out), a page id outside      */
@@ -501,7 +502,7 @@ kvz_status kvz_expand_int4(const void* cache, int64_t n_pages, int page_size, co
                            const int64_t* offsets, int64_t B, int d, void* K_out, void* V_out,
                            int64_t n_rows, int32_t* d_status, cudaStream_t stream);
 
-size_t kvz_decode_int4_workspace_size(int G, int d);
+size_t kvz_decode_int4_workspace_size(int64_t B, int G, int64_t rows, int d);
 
 kvz_status kvz_decode_int4(const void* q, const void* cache, int64_t n_pages, int page_size,
                            const int32_t* pages, int64_t max_pages, const int32_t* counts, int64_t B,

@@ -98,7 +98,7 @@ _SIGS = {
                                _vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp,
                                _vp]),
     "kvz_expand_int4": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp]),
-    "kvz_decode_int4_workspace_size": (_sz, [_i32, _i32]),
+    "kvz_decode_int4_workspace_size": (_sz, [_i64, _i32, _i64, _i32]),
     "kvz_decode_int4": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp,
                                _vp]),
     "kvz_testing_compact_in_place_withhold": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _i64, _i64,
@@ -122,7 +122,29 @@ def lib():
             fn.restype = res
             fn.argtypes = args
         _lib = handle
+        _load_fast()
     return _lib
+
+
+# The short way into the decoding calls (csrc/fast_calls.cpp), once the library
+# is loaded and if the module was built for this torch: same checks, same C
+# calls, same results, less host time.  It answers None for anything unusual,
+# which then goes through the checks below.
+_fast = None
+
+
+def _load_fast():
+    global _fast
+    try:
+        from . import _kvz_fast as m
+    except ImportError:
+        return
+    if m.torch_version != torch.__version__:
+        return
+    m.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in
+             ("kvz_rotary", "kvz_compact_int4", "kvz_append_int4", "kvz_expand_int4", "kvz_decode_int4",
+              "kvz_decode_int4_workspace_size")))
+    _fast = m
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -792,6 +814,7 @@ def kvz_compact_int8(K, V, idx, counts, offsets, out_offsets=None, out_rows: Opt
 # Rotary positions and the paged 4-bit cache
 # ---------------------------------------------------------------------------
 _NULL = contextlib.nullcontext()
+_bf16, _f32, _i32t, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _on(fn: str, dev, stream):
@@ -799,7 +822,7 @@ def _on(fn: str, dev, stream):
     a ``stream`` of the caller's, that stream current too, so that outputs and
     scratch allocated by the call belong to the stream that uses them."""
     if stream is None:
-        return _NULL if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return _NULL if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     if stream.device != dev:
@@ -807,22 +830,63 @@ def _on(fn: str, dev, stream):
     return torch.cuda.stream(stream)
 
 
+def _raw(dev) -> int:
+    """The handle of the current stream of ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(fn: str, first, *ts):
+    """_device, with a short way for the common case (a decoding step makes
+    these calls once per layer, and its kernels take about as long)."""
+    i = first.get_device()
+    if i >= 0:
+        for t in ts:
+            if t is not None and t.get_device() != i:
+                break
+        else:
+            return first.device
+    return _device(fn, first, *ts)
+
+
+def _vec(fn: str, name: str, t, dtype, numel: int, required: bool = False):
+    """_req for a dense tensor of at least ``numel`` entries."""
+    if t is None:
+        if required:
+            raise ValueError("%s: %s is required" % (fn, name))
+        return
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()):
+        _req(fn, name, t, dtype, numel=numel)
+
+
+def _dense(fn: str, name: str, t, dtype, shape):
+    """_req for a dense tensor of exactly ``shape`` (None is accepted)."""
+    if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+                              t.is_contiguous()):
+        _req(fn, name, t, dtype, shape=shape)
+
+
 def _rows_view(fn: str, name: str, t, shape):
     """Check a bf16 tensor of rows whose last dimension is dense and whose
     other strides keep the rows 16-byte aligned; returns those strides."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s: %s must be a torch.Tensor" % (fn, name))
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _bf16:
         raise ValueError("%s: %s must be torch.bfloat16, got %s" % (fn, name, t.dtype))
     if t.shape != shape:
         raise ValueError("%s: %s must have shape %s, got %s" % (fn, name, tuple(shape), tuple(t.shape)))
-    *st, last = t.stride()
+    st = t.stride()
+    if st[-1] == 1 and not ((st[0] | st[1] | (st[2] if len(st) == 4 else 0)) & 7) and not t.data_ptr() & 15:
+        return st[:-1]
     # the stride of a dimension of one entry is never used
-    st = [0 if n == 1 else s for n, s in zip(t.shape, st)]
-    if last != 1 or any(s % 8 for s in st) or t.data_ptr() % 16:
+    use = tuple(0 if n == 1 else s for n, s in zip(t.shape, st[:-1]))
+    if st[-1] != 1 or any(s % 8 for s in use) or t.data_ptr() % 16:
         raise ValueError("%s: %s needs a dense last dimension, strides of a multiple of 8 and a 16-byte aligned base, "
-                         "got strides %s" % (fn, name, tuple(t.stride())))
-    return st
+                         "got strides %s" % (fn, name, st))
+    return use
 
 
 def _span(t):
@@ -915,7 +979,7 @@ def kvz_rotary_table(freqs, n_pos: int, factor: float = 1.0, table=None, stream=
     with _on(fn, dev, stream):
         if table is None:
             table = torch.empty((n_pos, rot), dtype=torch.float32, device=dev)
-        _check(fn, lib().kvz_rotary_table(_ptr(freqs), n_pos, rot, float(factor), _ptr(table), _stream(None)))
+        _check(fn, lib().kvz_rotary_table(_ptr(freqs), n_pos, rot, float(factor), _ptr(table), _raw(dev)))
     return table
 
 
@@ -923,11 +987,15 @@ def _rotation(fn, positions, table, B, n):
     """(pos stride, n_pos, rot) of checked positions [n] or [B, n] and table [n_pos, rot]."""
     if positions is None or table is None:
         raise ValueError("%s: positions and table go together" % fn)
-    _req(fn, "positions", positions, torch.int32)
-    if positions.shape != (n,) and positions.shape != (B, n):
-        raise ValueError("%s: positions must be [%d] or [%d, %d], got %s" % (fn, n, B, n, tuple(positions.shape)))
-    _req(fn, "table", table, torch.float32, ndim=2)
-    return (0 if positions.dim() == 1 else n), table.shape[0], table.shape[1]
+    _vec(fn, "positions", positions, _i32t, 0)
+    shape = positions.shape
+    if shape != (n,) and shape != (B, n):
+        raise ValueError("%s: positions must be [%d] or [%d, %d], got %s" % (fn, n, B, n, tuple(shape)))
+    _vec(fn, "table", table, _f32, 0)
+    if table.dim() != 2:
+        raise ValueError("%s: table must be [n_pos, rot], got %s" % (fn, tuple(table.shape)))
+    n_pos, rot = table.shape
+    return (0 if len(shape) == 1 else n), n_pos, rot
 
 
 def kvz_rotary(x, positions, table, interleaved: bool = False, inverse: bool = False, out=None, status=None,
@@ -941,29 +1009,32 @@ def kvz_rotary(x, positions, table, interleaved: bool = False, inverse: bool = F
     turn.  ``inverse`` turns the other way: the gradient of x for a gradient
     of out.  Nothing here is recorded for autograd."""
     fn = "kvz_rotary"
+    if _fast is not None and stream is None and out is None:
+        r = _fast.rotary(x, positions, table, interleaved, inverse, status)
+        if r is not None:
+            return r if type(r) is not int else _check(fn, r)
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError("%s: x must be bfloat16 [B, n, d] or [B, G, n, d]" % fn)
     shape = x.shape
     B, G, n, d = shape if len(shape) == 4 else (shape[0], 1, shape[1], shape[2])
     xs = _rows_view(fn, "x", x, shape)
     pos_sb, n_pos, rot = _rotation(fn, positions, table, B, n)
-    ys = None
     if out is not None:
         ys = _rows_view(fn, "out", out, shape)
         _distinct(fn, "out", out)
         if out.data_ptr() != x.data_ptr() or ys != xs:
             _apart(fn, "x", x, "out", out)
-    _status(fn, status)
-    dev = _device(fn, x, positions, table, out, status)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, x, positions, table, out, status)
     with _on(fn, dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            out = torch.empty(shape, dtype=_bf16, device=dev)
             ys = out.stride()[:-1]
         if len(shape) == 3:
             xs, ys = (xs[0], 0, xs[1]), (ys[0], 0, ys[1])
         _check(fn, lib().kvz_rotary(x.data_ptr(), *xs, B, G, n, d, positions.data_ptr(), pos_sb, table.data_ptr(), n_pos,
-                                    rot, int(bool(interleaved)), int(bool(inverse)), out.data_ptr(), *ys,
-                                    _ptr(status), _stream(None)))
+                                    rot, 1 if interleaved else 0, 1 if inverse else 0, out.data_ptr(), *ys,
+                                    _addr(status), _raw(dev)))
     return out
 
 
@@ -974,25 +1045,29 @@ def kvz_cache4_page_bytes(page_size: int, d: int) -> int:
 
 def _cache4(fn, cache, pages, page_size, d=None):
     """Check a page pool and table; returns (d, B)."""
-    if cache is None or pages is None:
-        raise ValueError("%s: cache and pages are required" % fn)
-    _req(fn, "cache", cache, torch.uint8, ndim=2)
-    _req(fn, "pages", pages, torch.int32, ndim=2)
-    if page_size < 16 or page_size > 1024 or page_size % 16:
+    _vec(fn, "cache", cache, _u8, 1, required=True)
+    _vec(fn, "pages", pages, _i32t, 0, required=True)
+    if page_size < 16 or page_size > 1024 or page_size & 15:
         raise ValueError("%s: page_size must be a multiple of 16 in [16, 1024], got %r" % (fn, page_size))
-    width = cache.shape[1]
+    width = cache.shape[-1]
     if d is None:
         d = 128 if width == page_size * 144 else 64
-    if d not in (64, 128):
+    if d != 64 and d != 128:
         raise ValueError("%s: head dimension must be 64 or 128, got %d" % (fn, d))
-    if width * 8 != page_size * d * 9 or cache.shape[0] < 1:
+    if width * 8 != page_size * d * 9 or cache.dim() != 2:
         raise ValueError("%s: cache must be [n_pages >= 1, %d] for page_size %d and d = %d, got %s"
                          % (fn, page_size * d * 9 // 8, page_size, d, tuple(cache.shape)))
-    if pages.shape[1] < 1:
-        raise ValueError("%s: pages must have a column at least" % fn)
-    if pages.shape[1] * page_size > 1 << 30:
+    shape = pages.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError("%s: pages must be [B, max_pages >= 1], got %s" % (fn, tuple(shape)))
+    if shape[1] * page_size > 1 << 30:
         raise ValueError("%s: a head's page table holds at most 2^30 rows" % fn)
-    return d, pages.shape[0]
+    return d, shape[0]
+
+
+def _table_rows(fn, pages_rows, B):
+    if pages_rows != B:
+        raise ValueError("%s: pages must have a row for each of the %d heads, got %d" % (fn, B, pages_rows))
 
 
 def kvz_compact_int4(K, V, idx, counts, offsets, cache, pages, page_size: int, status=None, stream=None):
@@ -1003,19 +1078,22 @@ def kvz_compact_int4(K, V, idx, counts, offsets, cache, pages, page_size: int, s
     [B, max_pages] are the caller's: every head needs pages for its rows, and
     no page may be named twice."""
     fn = "kvz_compact_int4"
+    if _fast is not None and stream is None:
+        r = _fast.compact(K, V, idx, counts, offsets, cache, pages, page_size, status)
+        if r is not None:
+            return r if type(r) is not int else _check(fn, r)
     B, n_c, d = _kv_pair(fn, K, V)
-    if idx is None or counts is None or offsets is None:
-        raise ValueError("%s: idx, counts and offsets are required" % fn)
-    _csr_args(fn, B, idx, counts, offsets)
+    _vec(fn, "idx", idx, _i32t, 0, required=True)
+    _vec(fn, "counts", counts, _i32t, B, required=True)
+    _vec(fn, "offsets", offsets, torch.int64, B + 1, required=True)
     page_size = int(page_size)
-    if _cache4(fn, cache, pages, page_size, d)[1] != B:
-        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
-    _status(fn, status)
-    dev = _device(fn, K, V, idx, counts, offsets, cache, pages, status)
+    _table_rows(fn, _cache4(fn, cache, pages, page_size, d)[1], B)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, K, V, idx, counts, offsets, cache, pages, status)
     with _on(fn, dev, stream):
-        _check(fn, lib().kvz_compact_int4(_ptr(K), _ptr(V), B, n_c, d, _ptr(idx), _ptr(counts), _ptr(offsets),
-                                          _ptr(cache), cache.shape[0], page_size, _ptr(pages), pages.shape[1],
-                                          _ptr(status), _stream(None)))
+        _check(fn, lib().kvz_compact_int4(K.data_ptr(), V.data_ptr(), B, n_c, d, idx.data_ptr(), counts.data_ptr(),
+                                          offsets.data_ptr(), cache.data_ptr(), cache.shape[0], page_size,
+                                          pages.data_ptr(), pages.shape[1], _addr(status), _raw(dev)))
     return cache
 
 
@@ -1031,45 +1109,50 @@ def kvz_append_int4(k, v, cache, pages, counts, page_size: int, positions=None, 
     and their q_out rows, stay as they were.  counts is not changed:
     counts_out holds the new lengths, for kvz_decode_int4."""
     fn = "kvz_append_int4"
+    if _fast is not None and stream is None:
+        r = _fast.append(k, v, cache, pages, counts, page_size, positions, table, interleaved, q, q_out, n_new,
+                         counts_out, status)
+        if r is not None:
+            return r if type(r) is not int else _check(fn, r)
     page_size = int(page_size)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("%s: k must be bfloat16 [B, T, d]" % fn)
-    B, T, d = k.shape
-    if _cache4(fn, cache, pages, page_size, d)[1] != B:
-        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
-    ks = _rows_view(fn, "k", k, k.shape)
-    vs = _rows_view(fn, "v", v, k.shape)
-    if counts is None:
-        raise ValueError("%s: counts is required" % fn)
-    _req(fn, "counts", counts, torch.int32, numel=B)
-    _req(fn, "n_new", n_new, torch.int32, numel=B)
-    _req(fn, "counts_out", counts_out, torch.int32, numel=B)
-    _apart(fn, "counts", counts, "counts_out", counts_out)
+    shape = k.shape
+    B, T, d = shape
+    _table_rows(fn, _cache4(fn, cache, pages, page_size, d)[1], B)
+    ks = _rows_view(fn, "k", k, shape)
+    vs = _rows_view(fn, "v", v, shape)
+    _vec(fn, "counts", counts, _i32t, B, required=True)
+    _vec(fn, "n_new", n_new, _i32t, B)
+    if counts_out is not None:
+        _vec(fn, "counts_out", counts_out, _i32t, B)
+        _apart(fn, "counts", counts, "counts_out", counts_out)
     pos_sb = n_pos = rot = 0
     if positions is not None or table is not None:
         pos_sb, n_pos, rot = _rotation(fn, positions, table, B, T)
     G, qs = 1, (0, 0, 0)
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != B or q.shape[2] != T or q.shape[3] != d:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("%s: q must be bfloat16 [%d, G, %d, %d]" % (fn, B, T, d))
         G = q.shape[1]
-        qs = _rows_view(fn, "q", q, q.shape)
-        _req(fn, "q_out", q_out, torch.bfloat16, shape=q.shape)
-        _apart(fn, "q", q, "q_out", q_out)
+        qs = _rows_view(fn, "q", q, (B, G, T, d))
+        if q_out is not None:
+            _dense(fn, "q_out", q_out, _bf16, (B, G, T, d))
+            _apart(fn, "q", q, "q_out", q_out)
     elif q_out is not None:
         raise ValueError("%s: q_out needs q" % fn)
-    _status(fn, status)
-    dev = _device(fn, k, v, cache, pages, counts, positions, table, q, q_out, n_new, counts_out, status)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, k, v, cache, pages, counts, positions, table, q, q_out, n_new, counts_out, status)
     with _on(fn, dev, stream):
         if counts_out is None:
-            counts_out = torch.empty(B, dtype=torch.int32, device=dev)
+            counts_out = torch.empty((B,), dtype=_i32t, device=dev)
         if q is not None and q_out is None:
-            q_out = torch.empty((B, G, T, d), dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty((B, G, T, d), dtype=_bf16, device=dev)
         _check(fn, lib().kvz_append_int4(
-            k.data_ptr(), *ks, v.data_ptr(), *vs, _ptr(q), *qs, _ptr(q_out), B, G, T, d, _ptr(positions), pos_sb,
-            _ptr(table), n_pos, rot, int(bool(interleaved)), cache.data_ptr(), cache.shape[0], page_size,
-            pages.data_ptr(), pages.shape[1], counts.data_ptr(), _ptr(n_new), counts_out.data_ptr(), _ptr(status),
-            _stream(None)))
+            k.data_ptr(), *ks, v.data_ptr(), *vs, _addr(q), *qs, _addr(q_out), B, G, T, d, _addr(positions), pos_sb,
+            _addr(table), n_pos, rot, 1 if interleaved else 0, cache.data_ptr(), cache.shape[0], page_size,
+            pages.data_ptr(), pages.shape[1], counts.data_ptr(), _addr(n_new), counts_out.data_ptr(), _addr(status),
+            _raw(dev)))
     return counts_out, q_out
 
 
@@ -1080,37 +1163,43 @@ def kvz_expand_int4(cache, pages, counts, offsets, page_size: int, first=None, o
     starting at offsets[b] (int64 [B + 1], as kvz_decode takes them).
     ``out_rows`` sizes freshly allocated outputs."""
     fn = "kvz_expand_int4"
+    if _fast is not None and stream is None and K_out is None and V_out is None:
+        r = _fast.expand(cache, pages, counts, offsets, page_size, first, out_rows, status)
+        if r is not None:
+            return r if type(r) is not int else _check(fn, r)
     page_size = int(page_size)
     d, B = _cache4(fn, cache, pages, page_size)
-    if counts is None or offsets is None:
-        raise ValueError("%s: counts and offsets are required" % fn)
-    _csr_args(fn, B, None, counts, offsets)
-    _req(fn, "first", first, torch.int32, numel=B)
+    _vec(fn, "counts", counts, _i32t, B, required=True)
+    _vec(fn, "offsets", offsets, torch.int64, B + 1, required=True)
+    _vec(fn, "first", first, _i32t, B)
     if out_rows is None and (K_out is None or V_out is None):
         raise ValueError("%s: out_rows is required without K_out and V_out" % fn)
     rows = K_out.shape[0] if out_rows is None else int(out_rows)
     if rows < 0:
         raise ValueError("%s: out_rows must not be negative" % fn)
-    for name, t in (("K_out", K_out), ("V_out", V_out)):
-        _rows_out(fn, name, t, torch.bfloat16, d, rows)
-    _apart(fn, "K_out", K_out, "V_out", V_out)
-    _status(fn, status)
-    dev = _device(fn, cache, pages, counts, first, offsets, K_out, V_out, status)
+    if K_out is not None or V_out is not None:
+        _rows_out(fn, "K_out", K_out, _bf16, d, rows)
+        _rows_out(fn, "V_out", V_out, _bf16, d, rows)
+        _apart(fn, "K_out", K_out, "V_out", V_out)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, cache, pages, counts, first, offsets, K_out, V_out, status)
     with _on(fn, dev, stream):
         if K_out is None:
-            K_out = torch.empty((rows, d), dtype=torch.bfloat16, device=dev)
+            K_out = torch.empty((rows, d), dtype=_bf16, device=dev)
         if V_out is None:
-            V_out = torch.empty((rows, d), dtype=torch.bfloat16, device=dev)
+            V_out = torch.empty((rows, d), dtype=_bf16, device=dev)
         if rows > 0:
             _check(fn, lib().kvz_expand_int4(
                 cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(), pages.shape[1], counts.data_ptr(),
-                _ptr(first), offsets.data_ptr(), B, d, K_out.data_ptr(), V_out.data_ptr(), rows, _ptr(status),
-                _stream(None)))
+                _addr(first), offsets.data_ptr(), B, d, K_out.data_ptr(), V_out.data_ptr(), rows, _addr(status),
+                _raw(dev)))
     return K_out, V_out
 
 
-def kvz_decode_int4_workspace_size(G: int, d: int) -> int:
-    return lib().kvz_decode_int4_workspace_size(int(G), int(d))
+def kvz_decode_int4_workspace_size(B: int, G: int, rows: int, d: int) -> int:
+    """Scratch bytes of kvz_decode_int4 for page tables of ``rows`` = max_pages
+    * page_size rows (0: it needs none)."""
+    return lib().kvz_decode_int4_workspace_size(int(B), int(G), int(rows), int(d))
 
 
 def kvz_decode_int4(q, cache, pages, counts, page_size: int, scale: Optional[float] = None, out=None, lse2=None,
@@ -1119,35 +1208,41 @@ def kvz_decode_int4(q, cache, pages, counts, page_size: int, scale: Optional[flo
     [B, G, d] fp32, lse2 [B, G] fp32).  q is bf16 [B, G, d]; cache, pages and
     counts are what kvz_compact_int4 and kvz_append_int4 fill."""
     fn = "kvz_decode_int4"
-    _req(fn, "q", q, torch.bfloat16, ndim=3)
-    if q is None:
-        raise ValueError("%s: q is required" % fn)
-    B, G, d = q.shape
+    if _fast is not None and stream is None:
+        r = _fast.decode(q, cache, pages, counts, page_size, scale, out, lse2, workspace, status)
+        if r is not None:
+            return r if type(r) is not int else _check(fn, r)
+    _vec(fn, "q", q, _bf16, 0, required=True)
+    if q.dim() != 3:
+        raise ValueError("%s: q must be [B, G, d], got %s" % (fn, tuple(q.shape)))
+    shape = q.shape
+    B, G, d = shape
     page_size = int(page_size)
-    if _cache4(fn, cache, pages, page_size, d)[1] != B:
-        raise ValueError("%s: pages must have a row for each of the %d heads" % (fn, B))
-    if counts is None:
-        raise ValueError("%s: counts is required" % fn)
-    _req(fn, "counts", counts, torch.int32, numel=B)
-    _req(fn, "out", out, torch.float32, shape=(B, G, d))
-    _req(fn, "lse2", lse2, torch.float32, shape=(B, G))
-    _req(fn, "workspace", workspace, torch.uint8)
-    _status(fn, status)
-    dev = _device(fn, q, cache, pages, counts, out, lse2, workspace, status)
+    _table_rows(fn, _cache4(fn, cache, pages, page_size, d)[1], B)
+    max_pages = pages.shape[1]
+    _vec(fn, "counts", counts, _i32t, B, required=True)
+    _dense(fn, "out", out, _f32, shape)
+    _dense(fn, "lse2", lse2, _f32, shape[:2])
+    _vec(fn, "workspace", workspace, _u8, 0)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, q, cache, pages, counts, out, lse2, workspace, status)
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        scale = d ** -0.5
     with _on(fn, dev, stream):
         if out is None:
-            out = torch.empty((B, G, d), dtype=torch.float32, device=dev)
+            out = torch.empty(shape, dtype=_f32, device=dev)
         if lse2 is None:
-            lse2 = torch.empty((B, G), dtype=torch.float32, device=dev)
+            lse2 = torch.empty((B, G), dtype=_f32, device=dev)
         if workspace is None:
-            workspace = torch.empty(max(1, lib().kvz_decode_int4_workspace_size(G, d)), dtype=torch.uint8, device=dev)
+            need = lib().kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d)
+            if need:
+                workspace = torch.empty((need,), dtype=_u8, device=dev)
         _check(fn, lib().kvz_decode_int4(q.data_ptr(), cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(),
-                                         pages.shape[1], counts.data_ptr(), B, G, d, scale, out.data_ptr(),
-                                         lse2.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
-                                         _stream(None)))
+                                         max_pages, counts.data_ptr(), B, G, d, scale, out.data_ptr(), lse2.data_ptr(),
+                                         _addr(workspace), 0 if workspace is None else workspace.numel(),
+                                         _addr(status), _raw(dev)))
     return out, lse2
+
 
 
 def kvz_testing_compact_in_place_withhold(K, V, idx, counts, offsets, wait_ns: int, hold_head: int,

@@ -6,6 +6,11 @@ Compiles every ``csrc/*.cu`` with ``-gencode arch=compute_100a,code=sm_100a``
 and links them into ``query_agnostic_kv_kvz_b200/libkvz.so``.  The CUDA
 runtime is linked statically; the driver's tensor-map encoder is looked up at
 run time, so the library needs no libcuda at link time.
+
+``csrc/fast_calls.cpp`` becomes ``_kvz_fast.so``, a CPython module for the
+installed torch that shortens the host's part of the decoding calls.  The
+binding works without it, only slower, so a machine that cannot compile it
+(no Python headers, say) is told and goes on.
 """
 from __future__ import annotations
 
@@ -53,8 +58,47 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+FAST_SRC = os.path.join(CSRC, "fast_calls.cpp")
+FAST = os.path.join(PKG, "_kvz_fast.so")
+FAST_STAMP = os.path.join(OBJDIR, "fast_calls.torch")
+
+
+def build_fast(force: bool = False, verbose: bool = False) -> bool:
+    """Compile (if stale) the host module; False where it cannot be compiled."""
+    import sysconfig
+
+    import torch
+    stamp = "%s %s" % (torch.__version__, sys.version)
+    if not force and os.path.exists(FAST) and os.path.exists(FAST_STAMP) and open(FAST_STAMP).read() == stamp and \
+            all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in (FAST_SRC, os.path.join(INCLUDE, "kvz.h"))):
+        return True
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = FAST + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-DKVZ_TORCH_VERSION=\"%s\"" % torch.__version__,
+           "-I" + os.path.join(t, "include"), "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-I" + INCLUDE, FAST_SRC,
+           "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    try:
+        subprocess.run(cmd, check=True)
+    except (OSError, subprocess.CalledProcessError) as e:
+        print("kvz: %s not built (%s); the decoding calls take their slower way on the host" % (FAST, e),
+              file=sys.stderr)
+        return False
+    os.replace(tmp, FAST)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(FAST_STAMP, "w") as f:
+        f.write(stamp)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libkvz.so."""
+    build_fast(force, verbose)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

@@ -53,10 +53,6 @@ constexpr int kD4Warps = 8;
 constexpr int kD4Threads = kD4Warps * 32;
 constexpr int kD4Stages = 2;
 constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share is at least a stage per warp
-#ifndef KVZ_D4_CLUSTER_ROWS
-#define KVZ_D4_CLUSTER_ROWS 1024
-#endif
-constexpr int kD4ClusterRows = KVZ_D4_CLUSTER_ROWS;           // rows a CTA may have to read in the cluster form
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
 
@@ -742,10 +738,8 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
 
 template <int D>
 cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
-  // CTAs per head that fill the GPU once, at most a portable cluster
-  int C = 1;
-  while (C < 8 && 2 * C * a.B <= kD4Workers) C *= 2;
-  if (a.cap <= static_cast<int64_t>(C) * kD4ClusterRows) {
+  const int C = decode4_cluster(a.B, a.cap);
+  if (C > 0) {
     cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(D4<D>::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};

@@ -162,8 +162,9 @@ kvz_status kvz_append_int4(const void* k, int64_t k_sb, int64_t k_st, const void
   return kvz::launch_append_int4(d, a, stream) == cudaSuccess ? KVZ_OK : KVZ_ERR_CUDA;
 }
 
-size_t kvz_decode_int4_workspace_size(int G, int d) {
-  if (G < 1 || G > kvz::kDecGMax || (d != 64 && d != 128)) return 0;
+size_t kvz_decode_int4_workspace_size(int64_t B, int G, int64_t rows, int d) {
+  if (B < 1 || B > 65535 || G < 1 || G > kvz::kDecGMax || (d != 64 && d != 128) || rows < 1) return 0;
+  if (kvz::decode4_cluster(B, rows) > 0) return 0;
   const size_t w = kvz::kD4Workers;
   return up256(w * sizeof(int4)) + up256(2 * w * 8 * sizeof(float2)) + up256(2 * w * G * d * sizeof(float));
 }
@@ -179,7 +180,8 @@ kvz_status kvz_decode_int4(const void* q, const void* cache, int64_t n_pages, in
   if (G < 1 || G > kvz::kDecGMax) return KVZ_ERR_UNSUPPORTED;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return KVZ_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4) || !aligned(lse2, 4)) return KVZ_ERR_ALIGNMENT;
-  if (workspace == nullptr || workspace_bytes < kvz_decode_int4_workspace_size(G, d)) return KVZ_ERR_WORKSPACE;
+  const size_t need = kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KVZ_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return KVZ_ERR_ALIGNMENT;
   a.B = B, a.G = G;
   a.cap = max_pages * page_size;

@@ -239,6 +239,19 @@ struct Dec4Args {
   float* part_o;                            // [2 * kD4Workers][G][d]
   int32_t* status;
 };
+// The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
+// table holds `cap` rows, or 0 for shares of equal work.  A cluster costs less
+// to start and join (us for 64 heads of 1,000 rows 10 against 17; of 8,000
+// rows 26 against 32; one head of 4,000 rows 9.1 against 10.3), shares cost
+// less where few CTAs, or a head far longer than the rest, would carry all (one
+// head of 8,000 rows 10.6 against 12.4, of 32,000 rows 14 against 30).  Lengths
+// are on the device, so the table's width stands for the longest head.
+inline int decode4_cluster(int64_t B, int64_t cap) {
+  int c = 1;
+  while (c < 8 && 2 * c * B <= kD4Workers) c *= 2;            // fill the GPU once, at most a portable cluster
+  const int64_t rows = 2 * c * B >= kD4Workers ? 2048 : 1024; // a CTA's rows at most (half or more of the GPU, or less)
+  return cap <= c * rows ? c : 0;
+}
 cudaError_t launch_decode_int4(int d, const Dec4Args& a, cudaStream_t stream);
 
 }  // namespace kvz

@@ -298,6 +298,15 @@ def test_decode_many_heads():
     check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
 
 
+def test_decode_many_heads_and_a_long_one():
+    # the same with a head long enough for shares of equal work: most CTAs begin, hold and end several heads
+    counts = [(n * 7) % 40 if n % 3 else 0 for n in range(1500)]
+    counts[700] = 9000
+    cache, pages, n, _, _ = filled(counts, 64, 16, 12)
+    assert kvz.kvz_decode_int4_workspace_size(1500, 2, pages.shape[1] * 16, 64) > 0
+    check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
+
+
 def test_decode_all_empty():
     cache, pages, n, _, _ = filled([0, 0, 0], 128, 16, 13)
     check_decode(rand((3, 4, 128), 3), cache, pages, n, 16, 0.1)
@@ -361,7 +370,9 @@ def test_decode_shared_pages():
 def test_decode_is_deterministic_and_leaves_inputs():
     cache, pages, n, _, _ = filled([5000, 40, 9000, 123], 128, 64, 23)
     q, c0 = rand((4, 8, 128), 24), cache.clone()
-    ws = torch.full((kvz.kvz_decode_int4_workspace_size(8, 128),), 255, dtype=torch.uint8, device="cuda")
+    need = kvz.kvz_decode_int4_workspace_size(4, 8, pages.shape[1] * 64, 128)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     a = kvz.kvz_decode_int4(q, cache, pages, n, 64, workspace=ws)
     for _ in range(3):
         b = kvz.kvz_decode_int4(q, cache, pages, n, 64, workspace=ws)
@@ -481,6 +492,62 @@ def test_compact_reports_bad_idx_and_counts():
     assert torch.equal(cache[p1], c0[p1]) and not torch.equal(cache[pages[0].long()], c0[pages[0].long()])
 
 
+def test_short_and_long_way_on_the_host_agree(monkeypatch):
+    # the same calls with and without the host module: results, given outputs, refusals and their codes
+    assert kvz._fast is not None, "csrc/fast_calls.cpp is not built"
+    B, T, G, d, page = 3, 5, 2, 64, 16
+    t = table(d, 300)
+    pos = torch.randint(0, 300, (B, T), dtype=torch.int32, device="cuda")
+    k, v, q = rand((B, T, d), 1), rand((T, B, d), 2).permute(1, 0, 2), rand((B, G, T, d), 3)
+    one = torch.arange(T, dtype=torch.int32, device="cuda")
+    n_new = torch.tensor([5, 0, 2], dtype=torch.int32, device="cuda")
+    K = rand((B, 40, d), 4)
+    idx = torch.arange(10, dtype=torch.int32, device="cuda").repeat(B)
+
+    def run():
+        st = new_status()
+        cache, pages = pool([20] * B, d, page, 9)
+        ten = torch.full((B,), 10, dtype=torch.int32, device="cuda")
+        res = [kvz.kvz_compact_int4(K, K, idx, ten, offsets_of([10] * B), cache, pages, page, status=st)]
+        n_out, q_out = torch.zeros_like(ten), torch.zeros((B, G, T, d), dtype=torch.bfloat16, device="cuda")
+        got = kvz.kvz_append_int4(k, v, cache, pages, ten, page, positions=pos, table=t, interleaved=True, q=q,
+                                  q_out=q_out, n_new=n_new, counts_out=n_out, status=st)
+        assert got[0] is n_out and got[1] is q_out
+        res += [*got, *kvz.kvz_append_int4(k[:, :1], v[:, :1], cache, pages, n_out, page)[:1]]
+        res += kvz.kvz_expand_int4(cache, pages, n_out, offsets_of(n_out.tolist()), page, first=None,
+                                   out_rows=int(n_out.sum()), status=st)
+        out = torch.empty((B, G, d), device="cuda")
+        got = kvz.kvz_decode_int4(q_out[:, :, 0].contiguous(), cache, pages, n_out, page, out=out, status=st)
+        assert got[0] is out
+        res += [*got, *kvz.kvz_decode_int4(q_out[:, :, 0].contiguous(), cache, pages, n_out, page, scale=0.25)]
+        res += [kvz.kvz_rotary(q, one, t, inverse=True), kvz.kvz_rotary(v, pos, t, interleaved=True, status=st)]
+        assert st.item() == 0
+        bad = []
+        for call in (lambda: kvz.kvz_append_int4(k, v, cache, pages, ten, page, positions=one, table=t[:, :24]),
+                     lambda: kvz.kvz_append_int4(k, v, cache, pages, ten, page, counts_out=ten),
+                     lambda: kvz.kvz_append_int4(k, v, cache, pages, ten, page, q=q, q_out=q),
+                     lambda: kvz.kvz_append_int4(k, v.cpu(), cache, pages, ten, page),
+                     lambda: kvz.kvz_rotary(q, one, t[:, :40].contiguous()),
+                     lambda: kvz.kvz_rotary(q, one[:4], t),
+                     lambda: kvz.kvz_decode_int4(rand((B, 9, d), 1), cache, pages, ten, page),
+                     lambda: kvz.kvz_decode_int4(rand((B, 2, d), 1), cache, pages, ten, page, scale=-1.0),
+                     lambda: kvz.kvz_decode_int4(rand((B, 2, d), 1), cache, pages, ten, 24),
+                     lambda: kvz.kvz_expand_int4(cache, pages, ten, offsets_of([10] * B), page),
+                     lambda: kvz.kvz_compact_int4(K, K, idx, ten, offsets_of([10] * B), cache, pages[:2], page)):
+            with pytest.raises((ValueError, kvz.KvzError)) as e:
+                call()
+            bad.append((type(e.value), getattr(e.value, "code", None)))
+        return res, bad
+
+    quick, bad = run()
+    monkeypatch.setattr(kvz, "_fast", None)
+    slow, bad2 = run()
+    assert bad == bad2
+    for a, b in zip(quick, slow):
+        assert a.dtype == b.dtype and a.shape == b.shape
+        assert torch.equal(a.view(torch.uint8) if a.is_contiguous() else a, b.view(torch.uint8) if b.is_contiguous() else b)
+
+
 # ---------------------------------------------------------------------------
 # Streams, graphs, and the whole path
 # ---------------------------------------------------------------------------
@@ -503,17 +570,19 @@ def test_streams():
 def test_decoding_in_graphs_that_share_a_workspace():
     # one graph appends, another attends, a third attends over another cache with the same workspace; replayed in turn
     d, page, B, G = 128, 16, 3, 4
-    counts = [100, 7, 250]
+    counts = [100, 7, 9250]
     cache, pages = pool([c + 8 for c in counts], d, page, 5)
-    k0, v0 = rand((B, 250, d), 40), rand((B, 250, d), 41)
+    k0, v0 = rand((B, 9250, d), 40), rand((B, 9250, d), 41)
     zero = torch.zeros(B, dtype=torch.int32, device="cuda")
     n0 = torch.tensor(counts, dtype=torch.int32, device="cuda")
     kvz.kvz_append_int4(k0, v0, cache, pages, zero, page, n_new=n0)
-    other = filled([33, 500, 1], d, page, 42)
-    ws = torch.empty(kvz.kvz_decode_int4_workspace_size(G, d), dtype=torch.uint8, device="cuda")
+    other = filled([33, 12000, 1], d, page, 42)
+    need = kvz.kvz_decode_int4_workspace_size(B, G, pages.shape[1] * page, d)
+    assert need == kvz.kvz_decode_int4_workspace_size(B, G, other[1].shape[1] * page, d) > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     cnt, nxt = n0.clone(), n0.clone()
     k, v, q = rand((B, 1, d), 43), rand((B, 1, d), 44), rand((B, G, 1, d), 45)
-    t = table(d, 400)
+    t = table(d, 9400)
     pos = n0[:, None].clone()
     q_out = torch.empty_like(q)
     out, lse2 = torch.empty((B, G, d), device="cuda"), torch.empty((B, G), device="cuda")

@@ -224,10 +224,10 @@ def test_c_expand_refuses(lib, kw, code):
     (dict(q=None), INVALID), (dict(counts=None), INVALID), (dict(out=None), INVALID), (dict(G=0), UNSUPPORTED),
     (dict(G=9), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(q=P + 8), ALIGNMENT),
     (dict(out=P + 4), ALIGNMENT), (dict(lse2=P + 1), ALIGNMENT), (dict(ws=None), WORKSPACE), (dict(ws_bytes=100), WORKSPACE),
-    (dict(ws=P + 16), ALIGNMENT)])
+    (dict(ws=P + 16), ALIGNMENT), (dict(n_pages=0x7FFFFFFF), INVALID)])
 def test_c_decode_refuses(lib, kw, code):
-    a = dict(q=P, **PAGES, counts=P, B=1, G=2, d=64, scale=0.125, out=P, lse2=P, ws=P, ws_bytes=1 << 24, st=None,
-             stream=None)
+    a = dict(q=P, **{**PAGES, "max_pages": 5000}, counts=P, B=1, G=2, d=64, scale=0.125, out=P, lse2=P, ws=P,
+             ws_bytes=1 << 24, st=None, stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
     assert lib.kvz_decode_int4(*a.values()) == code
@@ -237,8 +237,10 @@ def test_sizes(lib):
     assert lib.kvz_cache4_page_bytes(64, 128) == 64 * 144 and lib.kvz_cache4_page_bytes(16, 64) == 16 * 72
     for bad in ((0, 128), (24, 128), (2048, 64), (64, 96)):
         assert lib.kvz_cache4_page_bytes(*bad) == 0
-    assert lib.kvz_decode_int4_workspace_size(0, 128) == 0 and lib.kvz_decode_int4_workspace_size(9, 64) == 0
-    assert lib.kvz_decode_int4_workspace_size(8, 128) > 2 * 296 * 8 * 128 * 4
+    size = lib.kvz_decode_int4_workspace_size
+    assert size(0, 4, 1 << 20, 128) == 0 and size(4, 9, 1 << 20, 64) == 0 and size(4, 4, 1 << 20, 96) == 0
+    assert size(64, 8, 1 << 20, 128) > 2 * 296 * 8 * 128 * 4
+    assert size(8, 4, 100, 128) == 0                  # short heads need no scratch
 
 
 def test_page_division_is_exact():
