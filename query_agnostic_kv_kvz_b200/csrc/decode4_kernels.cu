@@ -142,72 +142,110 @@ __device__ __forceinline__ int64_t blocks_of(int c, int64_t cap) {
   return c < 0 || c > cap ? 0 : (c + kC4Rows - 1) / kC4Rows;
 }
 
-// Sum over the CTA, in every thread.
-__device__ __forceinline__ int64_t cta_sum(int64_t v, int64_t* s_red) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+// Inclusive scan over the CTA's threads; returns the sum.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t& inc, int64_t* s_red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFullMask, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();                                            // the last scan's sums are read
+  if (lane == 31) s_red[warp] = inc;
   __syncthreads();
-  int64_t t = 0;
-  for (int i = 0; i < kD4Warps; ++i) t += s_red[i];
-  __syncthreads();
-  return t;
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kD4Warps; ++i) {
+    if (i < warp) inc += s_red[i];
+    all += s_red[i];
+  }
+  return all;
 }
 
-// One part of a head, blocks [a0, a1) of head b's `count` rows, read by the
-// CTA's warps 32 rows at a time; each leaves its reference, sum and output per
-// query in shared memory.  False in a warp whose wait expired.
+// Blocks [a0, a1) of head b's `count` rows; none: b < 0.  Its 32-row stages go
+// to the CTA's warps in turn.
+struct Part4 {
+  int b, count, a0, a1;
+  __device__ __forceinline__ int stages(int warp) const {
+    const int n = b < 0 ? 0 : (a1 - a0 + 1) / 2;
+    return n > warp ? (n - warp + kD4Warps - 1) / kD4Warps : 0;
+  }
+  __device__ __forceinline__ int block(int warp, int i) const { return a0 + 2 * (warp + kD4Warps * i); }
+};
+
+// A warp's ring of stages, kept full across the parts that its CTA reads one
+// after another.  Where stages lie in the pool is looked up 32 at a time, a
+// lane each.
 template <int D>
-__device__ __forceinline__ bool read_part(const Dec4Args& p, int64_t b, int count, int a0, int a1, uint8_t* ring,
-                                          uint64_t* bar, uint32_t& used, volatile int* abort_flag, float* s_o,
-                                          float (*s_m)[8], float (*s_l)[8]) {
+struct Ring4 {
+  uint8_t* ring;
+  uint64_t* bar;
+  uint32_t used;                                              // stages taken
+  int issued;                                                 // of the current part's (and then the next one's) stages
+  int at0, at1;                                               // pool blocks of stage lane, lane + 32, ...
+
+  __device__ __forceinline__ void look_up(const Dec4Args& p, const Part4& t, int warp, int i) {
+    if (i >= t.stages(warp)) return;
+    const uint32_t blk = static_cast<uint32_t>(t.block(warp, i));
+    const uint32_t pi0 = page_of(p.pg, blk);
+    const uint32_t pi1 = static_cast<int>(blk) + 1 < t.a1 ? page_of(p.pg, blk + 1) : pi0;
+    const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(t.b) * p.pg.max_pages;
+    int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
+    if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
+      report(p.status, KVZ_ERR_INVALID_ARG);                  // page 0 stands in, so the read stays inside
+      id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
+      id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
+    }
+    at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(blk - pi0 * p.pg.blocks);
+    at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
+  }
+  // Issue the copies of stage i of part t, `ahead` stages past the one now due.
+  __device__ __forceinline__ void issue(const Dec4Args& p, const Part4& t, int warp, int lane, int i, int ahead) {
+    using L = C4<D>;
+    if ((i & 31) == 0) look_up(p, t, warp, i + lane);
+    const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
+    if (lane == 0) {
+      const uint32_t st = (used + static_cast<uint32_t>(ahead)) % kD4Stages;
+      uint8_t* const dst = ring + st * D4<D>::STAGE;
+      const bool two = t.block(warp, i) + 1 < t.a1, joined = two && from1 == from0 + 1;
+      mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
+      bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
+      if (two && !joined)
+        bulk_load(dst + L::BLOCK, p.pg.cache + static_cast<int64_t>(from1) * L::BLOCK, L::BLOCK, &bar[st]);
+    }
+  }
+  // The next stage that is not under way: of part t (n stages), then of the part after it (all - n), which lies in
+  // shared memory since it is looked at so rarely.
+  __device__ __forceinline__ void issue_next(const Dec4Args& p, const Part4& t, const Part4* then, int n, int warp,
+                                             int lane, int ahead) {
+    if (issued < n) issue(p, t, warp, lane, issued, ahead);
+    else issue(p, *then, warp, lane, issued - n, ahead);
+    ++issued;
+  }
+  // Let the copies under way land (bounded), behind `taken` stages done with, before the CTA leaves early.
+  __device__ __forceinline__ void drain(int lane, int taken) {
+    if (lane == 0)
+      for (int k = 0; k < issued - taken; ++k)
+        mbar_wait_for(&bar[(used + k) % kD4Stages], ((used + k) / kD4Stages) & 1u, 20000000ull);
+  }
+};
+
+// One part of a head, read by the CTA's warps 32 rows at a time; each leaves its
+// reference, sum and output per query in shared memory.  `then` (in shared
+// memory) is the part that the CTA reads next.  False in a warp whose wait
+// expired.
+template <int D>
+__device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, const Part4* then, Ring4<D>& q,
+                                          volatile int* abort_flag, float* s_o, float (*s_m)[8], float (*s_l)[8]) {
   using L = C4<D>;
   using S = D4<D>;
   constexpr int NG = L::NG;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int G = p.G;
-  const int n_st = (a1 - a0 + 1) / 2;                       // 32-row stages of this part; warp w takes w, w + 8, ...
-  const int n = n_st > warp ? (n_st - warp + kD4Warps - 1) / kD4Warps : 0;
-  auto blk_of = [&](int i) -> int { return a0 + 2 * (warp + kD4Warps * i); };
-
-  // The warp keeps its ring full.  Where its stages lie in the pool is looked up
-  // 32 stages at a time, a lane each (block numbers of the stage's two blocks).
-  int at0 = 0, at1 = 0;
-  auto look_up = [&](int i0) {
-    const int i = i0 + lane;
-    if (i < n) {
-      const uint32_t blk = static_cast<uint32_t>(blk_of(i));
-      const uint32_t pi0 = page_of(p.pg, blk);
-      const uint32_t pi1 = static_cast<int>(blk) + 1 < a1 ? page_of(p.pg, blk + 1) : pi0;
-      const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(b) * p.pg.max_pages;
-      int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
-      if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
-        report(p.status, KVZ_ERR_INVALID_ARG);              // page 0 stands in, so the read stays inside
-        id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
-        id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
-      }
-      const uint32_t in0 = blk - pi0 * p.pg.blocks;
-      at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(in0);
-      at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
-    }
-  };
-  auto issue = [&](int i, uint32_t ahead) {                 // `ahead`: how far past the stage now taken
-    const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
-    if (lane == 0) {
-      const uint32_t st = (used + ahead) % kD4Stages;
-      uint8_t* dst = ring + st * S::STAGE;
-      const bool two = blk_of(i) + 1 < a1, joined = two && from1 == from0 + 1;
-      mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
-      bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
-      if (two && !joined)
-        bulk_load(dst + L::BLOCK, p.pg.cache + static_cast<int64_t>(from1) * L::BLOCK, L::BLOCK, &bar[st]);
-    }
-  };
-  __syncthreads();                                          // barriers are initialised; s_o of the last part is read
-  look_up(0);
-#pragma unroll
-  for (int i = 0; i < kD4Stages; ++i)
-    if (i < n) issue(i, i);                                 // warp-uniform
+  const int n = part.stages(warp), all = n + then->stages(warp);
+  while (q.issued < kD4Stages && q.issued < all) q.issue_next(p, part, then, n, warp, lane, q.issued);   // warp-uniform
 
   // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
   // two to a largest exponent of 14; lane (r, c) loads query r and then works on
@@ -222,7 +260,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, int64_t b, int coun
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         v[g][u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (b * G + r) * D + 64 * g + 16 * c + 8 * u);
+        if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
         const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
@@ -268,14 +306,17 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, int64_t b, int coun
 
   bool ok = true;
   for (int i = 0; i < n; ++i) {
-    const uint32_t st = used % kD4Stages;
-    ok = mbar_wait_warp(&bar[st], (used / kD4Stages) & 1u, abort_flag, p.status);
-    if (!ok) break;                                         // warp-uniform
-    const uint8_t* stage = ring + st * S::STAGE;
-    const int blk0 = blk_of(i);
+    const uint32_t st = q.used % kD4Stages;
+    ok = mbar_wait_warp(&q.bar[st], (q.used / kD4Stages) & 1u, abort_flag, p.status);
+    if (!ok) {                                                // warp-uniform
+      q.drain(lane, i);
+      break;
+    }
+    const uint8_t* stage = q.ring + st * S::STAGE;
+    const int blk0 = part.block(warp, i);
     // rows of the stage that count: the head may end inside it, and this CTA's share after its first block (what
     // lies past them, in the page or left in the stage, has no influence)
-    const int rows = min(count - blk0 * kC4Rows, (a1 - blk0) * kC4Rows);
+    const int rows = min(part.count - blk0 * kC4Rows, (part.a1 - blk0) * kC4Rows);
 
     // ---- scores of keys 16k + 8h + r of the stage and queries 2c + e
     float x[2][2][2];                                       // [k][h][e]
@@ -426,20 +467,13 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, int64_t b, int coun
           for (int j = 0; j < 4; ++j) acc[j] += d[j];
         }
     }
-    __syncwarp();
-    if (i + kD4Stages < n) {                                // the stage is read: refill it
-      if (((i + kD4Stages) & 31) == 0) look_up(i + kD4Stages);
-      issue(i + kD4Stages, kD4Stages);
-    }
-    ++used;
+    __syncwarp();                                             // the stage is read
+    ++q.used;
+    if (q.issued < all) q.issue_next(p, part, then, n, warp, lane, kD4Stages - 1);
   }
-  if (!ok) {                                                // a wait expired: let this warp's own copies land
-    if (lane == 0)
-      for (int i = 0; i < kD4Stages; ++i) mbar_wait_for(&bar[(used + i) % kD4Stages], ((used + i) / kD4Stages) & 1u,
-                                                        20000000ull);
-  }
+  if (ok) q.issued -= n;                                      // the rest belongs to the next part
 
-  // ---- this head's part is read: the warps' states to shared memory
+  // ---- this head's part is read: the warps' states to shared memory (free again since the CTA's last barrier)
   const float s_out = s_top * 0x1p2f;                       // 2^E 2^-7 2^9
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -501,23 +535,26 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   __shared__ int s_cnt[kD4Counts];
   __shared__ int64_t s_red[kD4Warps];
   __shared__ int64_t s_find[2];                               // head that holds the first block, its first block
+  __shared__ Part4 s_then;
   __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G;
-  volatile int* abort_flag = &s_abort;
 
-  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
+  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);   // (the scan's barriers order this before its use)
   if (tid == 0) s_abort = 0;
   fence_mbar_init();
 
-  // ---- this CTA's share [u0, u1) of all heads' blocks
+  asm volatile("griddepcontrol.launch_dependents;");          // the merge may take its places as CTAs leave
+
+  // ---- this CTA's share [u0, u1) of all heads' blocks: their number, then the head that holds block u0
   int64_t mine = 0;
   for (int64_t b = tid; b < p.B; b += kD4Threads) {
     const int n = p.counts[b];
     if (b < kD4Counts) s_cnt[b] = n;
     mine += blocks_of(n, p.cap);
   }
-  const int64_t total = cta_sum(mine, s_red);
+  int64_t inc;                                                // blocks of the threads up to this one
+  int64_t total = cta_scan(mine, inc, s_red);
   int64_t quota = (total + kD4Workers - 1) / kD4Workers;
   quota = quota < kD4MinBlocks ? kD4MinBlocks : quota;
   const int64_t u0 = blockIdx.x * quota;
@@ -538,73 +575,76 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // the head that holds block u0: scan the heads' block counts, a CTA's width at a time
-  {
+  if (p.B <= kD4Threads) {                                    // a head per thread: the scan has it already
+    if (u0 >= inc - mine && u0 < inc) {
+      s_find[0] = tid;
+      s_find[1] = inc - mine;
+    }
+  } else {                                                    // again, a CTA's width of heads at a time
     int64_t carry = 0;
-    for (int64_t b0 = 0; b0 < p.B; b0 += kD4Threads) {
+    for (int64_t b0 = 0; b0 < p.B && carry <= u0; b0 += kD4Threads) {
       const int64_t b = b0 + tid;
       const int64_t n = b < p.B ? blocks_of(count_of(b), p.cap) : 0;
-      int64_t inc = n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(kFullMask, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) s_red[warp] = inc;
-      __syncthreads();
-      int64_t before = carry, all = 0;
-      for (int i = 0; i < kD4Warps; ++i) {
-        if (i < warp) before += s_red[i];
-        all += s_red[i];
-      }
-      const int64_t start = before + inc - n;
+      const int64_t all = cta_scan(n, inc, s_red);
+      const int64_t start = carry + inc - n;
       if (u0 >= start && u0 < start + n) {
         s_find[0] = b;
         s_find[1] = start;
       }
       carry += all;
-      __syncthreads();
-      if (carry > u0) break;                                  // uniform
     }
   }
-  int64_t b = s_find[0], start = s_find[1];
+  __syncthreads();
+  int64_t start = s_find[1];                                  // of the part's head
+  auto part_of = [&](int64_t b, int64_t at) -> Part4 {
+    const int count = count_of(b);
+    const int64_t n = blocks_of(count, p.cap);
+    return Part4{static_cast<int>(b), count, static_cast<int>(u0 > at ? u0 - at : 0), static_cast<int>(u1 - at < n ? u1 - at : n)};
+  };
+  Part4 part = part_of(s_find[0], start);
 
-  uint64_t* bar = full + warp * kD4Stages;
-  uint8_t* ring = smem + warp * (kD4Stages * S::STAGE);
+  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0};
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
-  uint32_t used = 0;                                          // stages this warp has taken from its ring
   int4 cont = make_int4(-1, 0, 0, 0);
 
   for (;;) {
-    const int count = count_of(b);
-    const int64_t n_blk = blocks_of(count, p.cap);
-    const int a0 = static_cast<int>(u0 > start ? u0 - start : 0);
-    const int a1 = static_cast<int>(u1 - start < n_blk ? u1 - start : n_blk);
-    const bool ok = read_part<D>(p, b, count, a0, a1, ring, bar, used, abort_flag, s_o, s_m, s_l);
-    const bool failed = __syncthreads_or(!ok);
-    if (failed) {                                             // uniform: the output of this share is not written
+    const int64_t n_blk = blocks_of(part.count, p.cap);
+    if (tid == 0) {
+      s_then.b = -1;
+      if (start + n_blk < u1) {                               // there is a next head: u1 <= total
+        int64_t nb = part.b;
+        do ++nb; while (blocks_of(count_of(nb), p.cap) == 0);
+        s_then = part_of(nb, start + n_blk);
+      }
+    }
+    __syncthreads();                                          // also: the warps' states of the last part are read
+    const bool ok = read_part<D>(p, part, &s_then, ring, &s_abort, s_o, s_m, s_l);
+    if (__syncthreads_or(!ok)) {                              // uniform: the output of this share is not written
+      if (ok) ring.drain(lane, 0);
       if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
       return;
     }
-    const bool whole = a0 == 0 && a1 == n_blk, past = a1 < n_blk;
+    const bool whole = part.a0 == 0 && part.a1 == n_blk, past = part.a1 < n_blk;
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (past ? 1 : 0);
     for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
       const int g = 4 * e4 / D;
       float M, Ls;
       const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
       if (whole) {
-        reinterpret_cast<float4*>(p.out + b * G * D)[e4] =
+        reinterpret_cast<float4*>(p.out + static_cast<int64_t>(part.b) * G * D)[e4] =
             make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + g] = M + log2f(Ls);
+        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[static_cast<int64_t>(part.b) * G + g] = M + log2f(Ls);
       } else {
         reinterpret_cast<float4*>(p.part_o + slot * G * D)[e4] = acc;
         if ((4 * e4) % D == 0) p.part_ml[slot * 8 + g] = make_float2(M, Ls);
       }
     }
-    if (a0 == 0 && past)                                      // this CTA begins the head, others go on with it
-      cont = make_int4(static_cast<int>(b), static_cast<int>((start + n_blk - 1) / quota), 0, 0);
-    if (start + n_blk >= u1) break;
+    if (part.a0 == 0 && past)                                 // this CTA begins the head, others go on with it
+      cont = make_int4(part.b, static_cast<int>((start + n_blk - 1) / quota), 0, 0);
+    if (s_then.b < 0) break;
     start += n_blk;
-    do ++b; while (blocks_of(count_of(b), p.cap) == 0);       // there is a next one: u1 <= total
+    part = s_then;
+    __syncthreads();                                          // s_then is read
   }
   if (tid == 0) p.cont[blockIdx.x] = cont;
 }
@@ -621,6 +661,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   __shared__ uint64_t full[kD4Warps * kD4Stages];
   __shared__ int s_abort;
   __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
+  __shared__ Part4 s_then;
   __shared__ float s_cm[8], s_cl[8];                          // this CTA's reference and sum per query
   __shared__ __align__(16) float s_co[8 * D];                 // and output
   const cg::cluster_group cluster = cg::this_cluster();
@@ -645,9 +686,10 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   const int a0 = 2 * static_cast<int>(static_cast<int64_t>(n_st) * rank / C);
   const int a1 = min(2 * static_cast<int>(static_cast<int64_t>(n_st) * (rank + 1) / C), n_blk);
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
-  uint32_t used = 0;
-  const bool ok = read_part<D>(p, b, count, a0, a1, smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, used,
-                               &s_abort, s_o, s_m, s_l);
+  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0};
+  if (tid == 0) s_then.b = -1;
+  __syncthreads();                                            // the barriers are initialised
+  const bool ok = read_part<D>(p, Part4{static_cast<int>(b), count, a0, a1}, &s_then, ring, &s_abort, s_o, s_m, s_l);
   const bool failed = __syncthreads_or(!ok);
   for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
     const int g = 4 * e4 / D;
@@ -681,58 +723,80 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
 
 // The heads that CTA blockIdx.x began and others went on with: their partials
 // (reference m, sum l, output o) join as M = max m, sum l 2^(m - M), sum o
-// 2^(m - M), in the CTAs' order.
+// 2^(m - M), in the CTAs' order.  Launched while the shares still run; what
+// they wrote is read after the wait, the first outputs before their weights
+// are known.
 template <int D>
 __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
   constexpr int C = D / 4, RS = kD4Threads / C;               // float4 columns, partials read side by side
+  constexpr int AHEAD = 4;
   __shared__ float s_w[kD4Workers];
   __shared__ float s_red[kD4Warps], s_red2[kD4Warps];
   __shared__ float4 s_acc[kD4Threads];
-  const int first = blockIdx.x, tid = threadIdx.x, G = p.G;
+  const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, G = p.G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 cont = p.cont[first];
   if (cont.x < 0) return;
   const int np = cont.y - first + 1;                          // CTAs first .. last: all but the last run past their range
   auto slot = [&](int i) -> int64_t { return 2 * static_cast<int64_t>(first + i) + (i + 1 < np ? 1 : 0); };
-  for (int g = blockIdx.y; g < G; g += gridDim.y) {
-    float M = -INFINITY, Ls = 0.0f;
-    for (int i = tid; i < np; i += kD4Threads) M = fmaxf(M, p.part_ml[slot(i) * 8 + g].x);
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[tid >> 5] = M;
-    __syncthreads();
-    for (int i = 0; i < kD4Warps; ++i) M = fmaxf(M, s_red[i]);
-    for (int i = tid; i < np; i += kD4Threads) {
-      const float2 ml = p.part_ml[slot(i) * 8 + g];
-      const float w = exp2f(ml.x - M);
+  const int col = tid % C, lanep = tid / C;
+  auto output = [&](int i) -> float4 {
+    return i < np ? reinterpret_cast<const float4*>(p.part_o + (slot(i) * G + g) * D)[col]
+                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  float2 ml[2];                                               // np <= kD4Workers <= 2 per thread
+  static_assert(kD4Workers <= 2 * kD4Threads, "");
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    ml[k] = tid + k * kD4Threads < np ? p.part_ml[slot(tid + k * kD4Threads) * 8 + g] : make_float2(-INFINITY, 0.0f);
+  float4 v[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) v[k] = output(lanep + k * RS);
+  float M = fmaxf(ml[0].x, ml[1].x);
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kD4Warps; ++i) M = fmaxf(M, s_red[i]);
+  float Ls = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * kD4Threads;
+    if (i < np) {
+      const float w = exp2f(ml[k].x - M);
       s_w[i] = w;
-      Ls = fmaf(ml.y, w, Ls);
+      Ls = fmaf(ml[k].y, w, Ls);
     }
-    for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFullMask, Ls, o);
-    if ((tid & 31) == 0) s_red2[tid >> 5] = Ls;
-    __syncthreads();
-    Ls = 0.0f;
-    for (int i = 0; i < kD4Warps; ++i) Ls += s_red2[i];
-    const int col = tid % C, lanep = tid / C;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = lanep; i < np; i += RS) {
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + (slot(i) * G + g) * D)[col];
-      const float w = s_w[i];
-      acc.x = fmaf(v.x, w, acc.x), acc.y = fmaf(v.y, w, acc.y);
-      acc.z = fmaf(v.z, w, acc.z), acc.w = fmaf(v.w, w, acc.w);
-    }
-    s_acc[tid] = acc;
-    __syncthreads();
-    if (tid < C) {
-      for (int i = 1; i < RS; ++i) {
-        const float4 v = s_acc[i * C + tid];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+  }
+  for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(kFullMask, Ls, o);
+  if ((tid & 31) == 0) s_red2[tid >> 5] = Ls;
+  __syncthreads();
+  Ls = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kD4Warps; ++i) Ls += s_red2[i];
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = lanep; i0 < np; i0 += AHEAD * RS) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + k * RS;
+      if (i < np) {
+        const float w = s_w[i];
+        acc.x = fmaf(v[k].x, w, acc.x), acc.y = fmaf(v[k].y, w, acc.y);
+        acc.z = fmaf(v[k].z, w, acc.z), acc.w = fmaf(v[k].w, w, acc.w);
       }
-      const int64_t at = static_cast<int64_t>(cont.x) * G + g;
-      reinterpret_cast<float4*>(p.out + at * D)[tid] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-      if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = M + log2f(Ls);
+      v[k] = output(i + AHEAD * RS);
     }
-    __syncthreads();
+  }
+  s_acc[tid] = acc;
+  __syncthreads();
+  if (tid < C) {
+    for (int i = 1; i < RS; ++i) {
+      const float4 x = s_acc[i * C + tid];
+      acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+    }
+    const int64_t at = static_cast<int64_t>(cont.x) * G + g;
+    reinterpret_cast<float4*>(p.out + at * D)[tid] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+    if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = M + log2f(Ls);
   }
 }
 
@@ -760,8 +824,16 @@ cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
   decode_int4_kernel<D><<<kD4Workers, kD4Threads, D4<D>::SMEM, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  merge_int4_kernel<D><<<dim3(kD4Workers, static_cast<unsigned>(a.G)), kD4Threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kD4Workers, static_cast<unsigned>(a.G));
+  cfg.blockDim = dim3(kD4Threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_int4_kernel<D>, a);
 }
 
 }  // namespace

