@@ -11,6 +11,7 @@
 #include "kvz.h"
 #include "kvz_cache4.cuh"
 #include "kvz_internal.h"
+#include "kvz_launch.cuh"
 #include "kvz_rotary.cuh"
 #include "kvz_sm100.cuh"
 
@@ -96,12 +97,14 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[2 * 
 
 template <int D>
 __global__ void __launch_bounds__(kC4Threads, 2)
-    compact_int4_kernel(const uint16_t* __restrict__ K, const uint16_t* __restrict__ V, int64_t B, int64_t n_c,
-                        const int32_t* __restrict__ idx, const int32_t* __restrict__ counts,
-                        const int64_t* __restrict__ offsets, Pages4 pg, int64_t cap, int32_t* status) {
+    compact_int4_kernel(const uint16_t* K, const uint16_t* V, int64_t B, int64_t n_c,
+                        const int32_t* idx, const int32_t* counts,
+                        const int64_t* offsets, Pages4 pg, int64_t cap, int32_t* status) {
   using L = C4<D>;
   constexpr int NG = L::NG;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  let_next_start();
+  after_prior(K, V, idx, counts, offsets, pg.cache, pg.pages);
   BlockWalk<1> h;
   h.run(offsets, B);
   if (h.u >= h.end) return;                                   // warp-uniform, as is all that follows per block
@@ -213,12 +216,14 @@ __global__ void __launch_bounds__(kC4Threads, 2)
 // A value is one fused bf16 multiply-add, s * code + m rounded once.
 template <int D>
 __global__ void __launch_bounds__(kC4Threads)
-    expand_int4_kernel(Pages4 pg, const int32_t* __restrict__ counts, const int32_t* __restrict__ first,
-                       const int64_t* __restrict__ offsets, int64_t B, int64_t cap, uint16_t* __restrict__ K_out,
-                       uint16_t* __restrict__ V_out, int64_t n_rows, int32_t* status) {
+    expand_int4_kernel(Pages4 pg, const int32_t* counts, const int32_t* first,
+                       const int64_t* offsets, int64_t B, int64_t cap, uint16_t* K_out,
+                       uint16_t* V_out, int64_t n_rows, int32_t* status) {
   using L = C4<D>;
   constexpr int NG = L::NG;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  let_next_start();
+  after_prior(pg.cache, pg.pages, counts, first, offsets, K_out, V_out);
   BlockWalk<2> h;
   h.run(offsets, B);
   if (h.u >= h.end) return;
@@ -373,6 +378,8 @@ __global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, 
   constexpr int PW = 16 / L::LPR;
   const int lane = threadIdx.x & 31, l = lane % L::LPR;
   int64_t w = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
+  let_next_start();
+  after_prior(a.k, a.v, a.q, a.rot.pos, a.rot.table, a.pg.cache, a.pg.pages, a.counts, a.n_new);
   const bool turning = a.rot.pos != nullptr;
 
   if (w < 2 * kv_warps) {
@@ -476,13 +483,8 @@ cudaError_t launch_compact_int4(const void* K, const void* V, int64_t B, int64_t
                                 cudaStream_t stream) {
   const uint16_t *k = static_cast<const uint16_t*>(K), *v = static_cast<const uint16_t*>(V);
   const unsigned grid = grid_for(B * (table_rows(pg) / kC4Rows + 1), kCompactCtas);   // (the counts are on the device)
-  if (d == 128)
-    compact_int4_kernel<128><<<grid, kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
-                                                                            table_rows(pg), status);
-  else
-    compact_int4_kernel<64><<<grid, kC4Threads, 0, stream>>>(k, v, B, n_c, idx, counts, offsets, pg,
-                                                                           table_rows(pg), status);
-  return cudaGetLastError();
+  return launch_after(d == 128 ? compact_int4_kernel<128> : compact_int4_kernel<64>, dim3(grid), dim3(kC4Threads), 0, stream,
+                      0, k, v, B, n_c, idx, counts, offsets, pg, table_rows(pg), status);
 }
 
 cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const int32_t* first, const int64_t* offsets,
@@ -490,13 +492,8 @@ cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const in
                                cudaStream_t stream) {
   uint16_t *k = static_cast<uint16_t*>(K_out), *v = static_cast<uint16_t*>(V_out);
   const unsigned grid = grid_for(n_rows / kC4Rows + 2 * B, kExpandCtas);
-  if (d == 128)
-    expand_int4_kernel<128><<<grid, kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
-                                                                           table_rows(pg), k, v, n_rows, status);
-  else
-    expand_int4_kernel<64><<<grid, kC4Threads, 0, stream>>>(pg, counts, first, offsets, B,
-                                                                          table_rows(pg), k, v, n_rows, status);
-  return cudaGetLastError();
+  return launch_after(d == 128 ? expand_int4_kernel<128> : expand_int4_kernel<64>, dim3(grid), dim3(kC4Threads), 0, stream, 0,
+                      pg, counts, first, offsets, B, table_rows(pg), k, v, n_rows, status);
 }
 
 cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream) {
@@ -507,13 +504,8 @@ cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream)
   const int64_t warps = 2 * kv_warps + q_warps + (a.counts_out == nullptr ? 0 : a.B);
   const int64_t grid = (warps * 32 + kC4Threads - 1) / kC4Threads;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (d == 128)
-    append_int4_kernel<128><<<static_cast<unsigned>(grid), kC4Threads, 0, stream>>>(a, n_pairs, kv_warps, q_warps,
-                                                                                    table_rows(a.pg));
-  else
-    append_int4_kernel<64><<<static_cast<unsigned>(grid), kC4Threads, 0, stream>>>(a, n_pairs, kv_warps, q_warps,
-                                                                                   table_rows(a.pg));
-  return cudaGetLastError();
+  return launch_after(d == 128 ? append_int4_kernel<128> : append_int4_kernel<64>, dim3(static_cast<unsigned>(grid)),
+                      dim3(kC4Threads), 0, stream, 0, a, n_pairs, kv_warps, q_warps, table_rows(a.pg));
 }
 
 }  // namespace kvz

@@ -41,6 +41,7 @@
 #include "kvz.h"
 #include "kvz_cache4.cuh"
 #include "kvz_internal.h"
+#include "kvz_launch.cuh"
 #include "kvz_sm100.cuh"
 
 namespace cg = cooperative_groups;
@@ -138,6 +139,18 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
+// Loads that stay behind the wait for the kernels before this one.
+__device__ __forceinline__ int load_int(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t cap) {
   return c < 0 || c > cap ? 0 : (c + kC4Rows - 1) / kC4Rows;
 }
@@ -191,7 +204,7 @@ struct Ring4 {
     const uint32_t pi0 = page_of(p.pg, blk);
     const uint32_t pi1 = static_cast<int>(blk) + 1 < t.a1 ? page_of(p.pg, blk + 1) : pi0;
     const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(t.b) * p.pg.max_pages;
-    int id0 = __ldg(row_pages + pi0), id1 = __ldg(row_pages + pi1);
+    int id0 = load_int(row_pages + pi0), id1 = load_int(row_pages + pi1);
     if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
       report(p.status, KVZ_ERR_INVALID_ARG);                  // page 0 stands in, so the read stays inside
       id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
@@ -260,7 +273,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         v[g][u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < G) v[g][u] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
+        if (r < G) v[g][u] = load_16(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
         const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
@@ -544,12 +557,13 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   if (tid == 0) s_abort = 0;
   fence_mbar_init();
 
-  asm volatile("griddepcontrol.launch_dependents;");          // the merge may take its places as CTAs leave
+  let_next_start();                                           // the merge may take its places as CTAs leave
+  after_prior();
 
   // ---- this CTA's share [u0, u1) of all heads' blocks: their number, then the head that holds block u0
   int64_t mine = 0;
   for (int64_t b = tid; b < p.B; b += kD4Threads) {
-    const int n = p.counts[b];
+    const int n = load_int(p.counts + b);
     if (b < kD4Counts) s_cnt[b] = n;
     mine += blocks_of(n, p.cap);
   }
@@ -559,7 +573,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   quota = quota < kD4MinBlocks ? kD4MinBlocks : quota;
   const int64_t u0 = blockIdx.x * quota;
   const int64_t u1 = u0 + quota < total ? u0 + quota : total;
-  auto count_of = [&](int64_t b) -> int { return b < kD4Counts ? s_cnt[b] : p.counts[b]; };
+  auto count_of = [&](int64_t b) -> int { return b < kD4Counts ? s_cnt[b] : load_int(p.counts + b); };
 
   // heads without rows get their outputs here, heads with a bad count a report
   for (int64_t b = blockIdx.x; b < p.B; b += kD4Workers) {
@@ -668,7 +682,12 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, G = p.G;
   const int64_t b = blockIdx.x / C;
-  const int count = p.counts[b];                              // the same in all CTAs of the cluster
+  let_next_start();
+  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
+  if (tid == 0) s_abort = 0;
+  fence_mbar_init();
+  after_prior();
+  const int count = load_int(p.counts + b);                   // the same in all CTAs of the cluster
   if (count <= 0 || count > p.cap) {
     if (rank == 0 && count == 0) {
       for (int e = tid; e < G * D; e += kD4Threads) p.out[b * G * D + e] = 0.0f;
@@ -678,9 +697,6 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     }
     return;
   }
-  if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
-  if (tid == 0) s_abort = 0;
-  fence_mbar_init();
   // parts in whole stages, so that only the head's last block can stand alone
   const int n_blk = (count + kC4Rows - 1) / kC4Rows, n_st = (n_blk + 1) / 2;
   const int a0 = 2 * static_cast<int>(static_cast<int64_t>(n_st) * rank / C);
@@ -734,7 +750,8 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
   __shared__ float s_red[kD4Warps], s_red2[kD4Warps];
   __shared__ float4 s_acc[kD4Threads];
   const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, G = p.G;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  after_prior();
   const int4 cont = p.cont[first];
   if (cont.x < 0) return;
   const int np = cont.y - first + 1;                          // CTAs first .. last: all but the last run past their range
@@ -806,34 +823,15 @@ cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
   if (C > 0) {
     cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(D4<D>::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(C);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B * C));
-    cfg.blockDim = dim3(kD4Threads);
-    cfg.dynamicSmemBytes = D4<D>::SMEM;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_int4_cluster_kernel<D>, a);
+    return launch_after(decode_int4_cluster_kernel<D>, dim3(static_cast<unsigned>(a.B * C)), dim3(kD4Threads),
+                        D4<D>::SMEM, stream, C, a);
   }
   cudaError_t e = smem_limit_once<decode_int4_kernel<D>>(D4<D>::SMEM);
   if (e != cudaSuccess) return e;
-  decode_int4_kernel<D><<<kD4Workers, kD4Threads, D4<D>::SMEM, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_after(decode_int4_kernel<D>, dim3(kD4Workers), dim3(kD4Threads), D4<D>::SMEM, stream, 0, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kD4Workers, static_cast<unsigned>(a.G));
-  cfg.blockDim = dim3(kD4Threads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_int4_kernel<D>, a);
+  return launch_after(merge_int4_kernel<D>, dim3(kD4Workers, static_cast<unsigned>(a.G)), dim3(kD4Threads), 0, stream, 0,
+                      a);
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 
 #include "kvz.h"
 #include "kvz_internal.h"
+#include "kvz_launch.cuh"
 #include "kvz_rotary.cuh"
 #include "kvz_sm100.cuh"
 
@@ -50,6 +51,8 @@ __global__ void __launch_bounds__(kRotThreads)
 template <int D, bool IL>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a, int heads, int64_t n_threads) {
   constexpr int IT = D / 16;                                    // items of a row
+  let_next_start();
+  after_prior(a.x, a.y, a.rot.pos, a.rot.table);
   const int64_t f = static_cast<int64_t>(blockIdx.x) * kRotThreads + threadIdx.x;
   if (f >= n_threads) return;
   const int item = static_cast<int>(f % IT);
@@ -129,14 +132,9 @@ cudaError_t launch_rotary(int d, const RotaryArgs& a, cudaStream_t stream) {
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(blocks);
   const int h = static_cast<int>(heads);
-  if (d == 128) {
-    if (a.rot.interleaved) rotary_kernel<128, true><<<grid, kRotThreads, 0, stream>>>(a, h, n);
-    else rotary_kernel<128, false><<<grid, kRotThreads, 0, stream>>>(a, h, n);
-  } else {
-    if (a.rot.interleaved) rotary_kernel<64, true><<<grid, kRotThreads, 0, stream>>>(a, h, n);
-    else rotary_kernel<64, false><<<grid, kRotThreads, 0, stream>>>(a, h, n);
-  }
-  return cudaGetLastError();
+  const auto kernel = d == 128 ? (a.rot.interleaved ? rotary_kernel<128, true> : rotary_kernel<128, false>)
+                               : (a.rot.interleaved ? rotary_kernel<64, true> : rotary_kernel<64, false>);
+  return launch_after(kernel, dim3(grid), dim3(kRotThreads), 0, stream, 0, a, h, n);
 }
 
 }  // namespace kvz
