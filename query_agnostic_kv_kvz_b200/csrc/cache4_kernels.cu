@@ -365,52 +365,79 @@ __device__ __forceinline__ void turn_row(uint4& x, int lane, int l, const RotArg
   }
 }
 
-// Append.  Warps take, in this order: K row pairs, V row pairs, query rows,
-// and one head each for the new counts.  Pair j of head b covers the slots
-// 2 (counts[b] / 2 + j) and the next, of which those in [counts[b], counts[b]
-// + n_new[b]) are written; a slot's other half and all later rows stay as
-// they were.  A single token is latency (the count, the page and the row one
-// after another), so K, V and queries go to warps of their own.
+// Append.  Warps take, in this order: one head each for the new counts (the
+// longest chain of loads), K row pairs, V row pairs, query rows.  Pair j of
+// head b covers the slots 2 (counts[b] / 2 + j) and the next, of which those
+// in [counts[b], counts[b] + n_new[b]) are written; a slot's other half and
+// all later rows stay as they were.  What a row needs is a chain of loads (its
+// head's count, then its page, position and values, then its angles), so a
+// single token is latency, and K, V and queries go to warps of their own; two
+// and four chains side by side in a warp were no faster on long prompts either.
 template <int D>
-__global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, int n_pairs, int64_t kv_warps,
-                                                                 int64_t q_warps, int64_t cap) {
+__global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, uint32_t n_warps, uint32_t n_pairs,
+                                                                 uint32_t kv_warps, uint32_t q_warps, int64_t cap) {
   using L = C4<D>;
   constexpr int PW = 16 / L::LPR;
   const int lane = threadIdx.x & 31, l = lane % L::LPR;
-  int64_t w = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
+  uint32_t w = (blockIdx.x * kC4Threads + threadIdx.x) >> 5;
   let_next_start();
   after_prior(a.k, a.v, a.q, a.rot.pos, a.rot.table, a.pg.cache, a.pg.pages, a.counts, a.n_new);
   const bool turning = a.rot.pos != nullptr;
 
+  if (w < n_warps) {
+    // the new count, if every page and position of the head's new rows is valid
+    const int64_t b = w, base = a.counts[b], len = a.n_new == nullptr ? a.T : a.n_new[b];
+    bool ok = base >= 0 && len >= 0 && len <= a.T && base + len <= cap;
+    if (ok && len > 0) {
+      const int64_t p0 = page_of(a.pg, static_cast<uint32_t>(base >> 4));
+      const int64_t p1 = page_of(a.pg, static_cast<uint32_t>((base + len - 1) >> 4));
+      int64_t worst = 0;                                      // the sign bit collects every bad id and position
+#pragma unroll 4
+      for (int64_t i = p0 + lane; i <= p1; i += 32) {
+        const int64_t id = a.pg.pages[b * a.pg.max_pages + i];
+        worst |= id | (a.pg.n_pages - 1 - id);
+      }
+      if (turning) {
+#pragma unroll 8
+        for (int64_t t = lane; t < len; t += 32) {
+          const int64_t p = a.rot.pos[b * a.rot.pos_sb + t];
+          worst |= p | (a.rot.n_pos - 1 - p);
+        }
+      }
+      ok = worst >= 0;
+    }
+    ok = __all_sync(kFullMask, ok);
+    if (lane == 0) a.counts_out[b] = static_cast<int32_t>(ok ? base + len : base);
+    return;
+  }
+  w -= n_warps;
   if (w < 2 * kv_warps) {
     const bool is_k = w < kv_warps;
     if (!is_k) w -= kv_warps;
     const int e = (lane / L::LPR) & 1, sub = lane / (2 * L::LPR);
-    const int64_t f = w * PW + sub, b = f / n_pairs;
-    const int j = static_cast<int>(f - b * n_pairs);
+    const uint32_t f = w * PW + sub, b = f / n_pairs, j = f - b * n_pairs;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     uint8_t* blk = nullptr;
     int row = e;
-    int64_t p = 0;
+    int32_t p = 0;
     if (b < a.B) {
-      const int64_t base = a.counts[b], len = a.n_new == nullptr ? a.T : a.n_new[b];
-      const bool head_ok = base >= 0 && len >= 0 && len <= a.T && base + len <= cap;
+      const int32_t base = a.counts[b], len = a.n_new == nullptr ? static_cast<int32_t>(a.T) : a.n_new[b];
+      const bool head_ok = base >= 0 && len >= 0 && len <= a.T && static_cast<int64_t>(base) + len <= cap;
       if (!head_ok && is_k && j == 0 && e == 0 && l == 0) report(a.status, KVZ_ERR_INVALID_ARG);
-      const int64_t slot = 2 * ((base >> 1) + j) + e, t = slot - base;
+      const int32_t slot = head_ok ? 2 * ((base >> 1) + static_cast<int32_t>(j)) + e : 0, t = slot - base;
       if (head_ok && t >= 0 && t < len) {
         x = is_k ? *reinterpret_cast<const uint4*>(a.k + b * a.k_sb + t * a.k_st + 8 * l)
                  : *reinterpret_cast<const uint4*>(a.v + b * a.v_sb + t * a.v_st + 8 * l);
-        blk = block_at<D>(a.pg, b, static_cast<uint32_t>(slot >> 4), a.status);
-        row = static_cast<int>(slot & 15);
-        if (turning) {
-          p = a.rot.pos[b * a.rot.pos_sb + t];
-          if (p < 0 || p >= a.rot.n_pos) {
-            report(a.status, KVZ_ERR_INVALID_ARG);
-            blk = nullptr;
-          }
-        }
+        if (turning) p = a.rot.pos[b * a.rot.pos_sb + t];
+        blk = block_at<D>(a.pg, b, static_cast<uint32_t>(slot) >> 4, a.status);
+        row = slot & 15;
       }
     }
+    if (turning && (p < 0 || p >= a.rot.n_pos)) {
+      report(a.status, KVZ_ERR_INVALID_ARG);
+      blk = nullptr;
+    }
+    if (!__any_sync(kFullMask, blk != nullptr)) return;
     uint32_t code[8], sm;
     if (is_k) {                                               // warp-uniform
       if (turning) turn_row<D>(x, lane, l, a.rot, p, blk != nullptr);
@@ -424,47 +451,43 @@ __global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, 
   }
   w -= 2 * kv_warps;
   if (w < q_warps) {
-    const int64_t f = w * (2 * PW) + lane / L::LPR;           // query row (b, g, t)
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    int64_t p = 0;
-    bool on = false;
-    if (f < a.B * a.G * a.T) {
-      const int64_t t = f % a.T, bg = f / a.T, b = bg / a.G;
-      const int g = static_cast<int>(bg - b * a.G);
-      const int64_t len = a.n_new == nullptr ? a.T : a.n_new[b];
-      if (t < len) {                                          // (a bad length is reported with the head's keys)
-        x = *reinterpret_cast<const uint4*>(a.q + b * a.q_sb + g * a.q_sg + t * a.q_st + 8 * l);
-        on = true;
-        if (turning) {
-          p = a.rot.pos[b * a.rot.pos_sb + t];
-          on = p >= 0 && p < a.rot.n_pos;
-        }
-      }
+    // a thread per 16 dims (whole pairs) of a token, all G rows of it by the same angles
+    constexpr uint32_t IT = D / 16;
+    const uint32_t f = w * 32 + lane, item = f % IT, bt = f / IT, T = static_cast<uint32_t>(a.T);
+    const uint32_t b = bt / T, t = bt - b * T;
+    if (b >= a.B || (a.n_new != nullptr && static_cast<int32_t>(t) >= a.n_new[b])) return;
+    const int rot = a.rot.rot, nrot = turning ? rot / 16 : 0;
+    const bool turn = static_cast<int>(item) < nrot, il = a.rot.interleaved != 0;
+    const int d0 = turn ? (il ? 16 * item : 8 * item) : (turning ? rot : 0) + 16 * (static_cast<int>(item) - nrot);
+    const int d1 = turn && !il ? d0 + rot / 2 : d0 + 8;
+    float c[8], s[8];
+    if (turning) {
+      const int32_t p = a.rot.pos[b * a.rot.pos_sb + t];
+      if (p < 0 || p >= a.rot.n_pos) return;                  // (reported with the head's keys)
+      if (turn) load_angles(a.rot.table + static_cast<int64_t>(p) * rot, rot / 2, 8 * item, 0, c, s);
     }
-    if (turning) turn_row<D>(x, lane, l, a.rot, p, on);
-    if (on) *reinterpret_cast<uint4*>(a.q_out + f * D + 8 * l) = x;
+    const uint16_t* const q = a.q + b * a.q_sb + t * a.q_st;
+    for (int g0 = 0; g0 < a.G; g0 += 4) {
+      uint4 v0[4], v1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (g0 + i < a.G) {
+          v0[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d0);
+          v1[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d1);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (g0 + i < a.G) {
+          if (turn) {
+            if (il) turn_adjacent(v0[i], v1[i], c, s);
+            else turn_halves(v0[i], v1[i], c, s);
+          }
+          uint16_t* const y = a.q_out + ((static_cast<int64_t>(b) * a.G + g0 + i) * T + t) * D;
+          *reinterpret_cast<uint4*>(y + d0) = v0[i];
+          *reinterpret_cast<uint4*>(y + d1) = v1[i];
+        }
+    }
     return;
-  }
-  w -= q_warps;
-  if (a.counts_out != nullptr && w < a.B) {
-    // the new count, if every page and position of the head's new rows is valid
-    const int64_t b = w, base = a.counts[b], len = a.n_new == nullptr ? a.T : a.n_new[b];
-    bool ok = base >= 0 && len >= 0 && len <= a.T && base + len <= cap;
-    if (ok && len > 0) {
-      const int64_t p0 = page_of(a.pg, static_cast<uint32_t>(base >> 4));
-      const int64_t p1 = page_of(a.pg, static_cast<uint32_t>((base + len - 1) >> 4));
-      for (int64_t i = p0 + lane; i <= p1; i += 32) {
-        const int32_t id = a.pg.pages[b * a.pg.max_pages + i];
-        ok = ok && id >= 0 && id < a.pg.n_pages;
-      }
-      if (turning)
-        for (int64_t t = lane; t < len; t += 32) {
-          const int64_t p = a.rot.pos[b * a.rot.pos_sb + t];
-          ok = ok && p >= 0 && p < a.rot.n_pos;
-        }
-    }
-    ok = __all_sync(kFullMask, ok);
-    if (lane == 0) a.counts_out[b] = static_cast<int32_t>(ok ? base + len : base);
   }
 }
 
@@ -497,15 +520,15 @@ cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const in
 }
 
 cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream) {
-  const int pw = 16 / (d / 8);                                // pairs per warp
-  const int n_pairs = static_cast<int>(a.T / 2 + 1);          // a run of T slots touches at most this many
+  const int64_t pw = 16 / (d / 8);                            // pairs per warp
+  const int64_t n_pairs = a.T / 2 + 1;                        // a run of T slots touches at most this many
+  const int64_t n_warps = a.counts_out == nullptr ? 0 : a.B;
   const int64_t kv_warps = (a.B * n_pairs + pw - 1) / pw;
-  const int64_t q_warps = a.q == nullptr ? 0 : (a.B * a.G * a.T + 2 * pw - 1) / (2 * pw);
-  const int64_t warps = 2 * kv_warps + q_warps + (a.counts_out == nullptr ? 0 : a.B);
-  const int64_t grid = (warps * 32 + kC4Threads - 1) / kC4Threads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int64_t q_warps = a.q == nullptr ? 0 : (a.B * a.T * (d / 16) + 31) / 32;
+  const int64_t grid = ((n_warps + 2 * kv_warps + q_warps) * 32 + kC4Threads - 1) / kC4Threads;
   return launch_after(d == 128 ? append_int4_kernel<128> : append_int4_kernel<64>, dim3(static_cast<unsigned>(grid)),
-                      dim3(kC4Threads), 0, stream, 0, a, n_pairs, kv_warps, q_warps, table_rows(a.pg));
+                      dim3(kC4Threads), 0, stream, 0, a, static_cast<uint32_t>(n_warps), static_cast<uint32_t>(n_pairs),
+                      static_cast<uint32_t>(kv_warps), static_cast<uint32_t>(q_warps), table_rows(a.pg));
 }
 
 }  // namespace kvz

@@ -137,8 +137,8 @@ kvz_status kvz_append_int4(const void* k, int64_t k_sb, int64_t k_st, const void
   kvz_status st = check_pages(cache, n_pages, page_size, pages, max_pages, B, d, &a.pg);
   if (st != KVZ_OK) return st;
   if (T < 1 || T > kMaxCacheRows || (q != nullptr && (G < 1 || G > 65535))) return KVZ_ERR_INVALID_ARG;
-  // pairs and query rows are numbered in 32 bits
-  if (B * (T / 2 + 1) > 0x7FFFFFFF || (q != nullptr && B * G > 0x7FFFFFFF / T)) return KVZ_ERR_INVALID_ARG;
+  // rows, and the warps that take them, are numbered in 32 bits
+  if (B * (T + 2) > (int64_t(1) << 28) || (q != nullptr && B * G > 0x7FFFFFFF / T)) return KVZ_ERR_INVALID_ARG;
   if (positions != nullptr) {
     st = check_rotation(positions, pos_sb, table, n_pos, rot, d, interleaved, 0, &a.rot);
     if (st != KVZ_OK) return st;
