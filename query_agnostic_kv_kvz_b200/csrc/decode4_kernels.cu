@@ -76,6 +76,23 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+// Two float32 operations in one instruction.
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c0, float c1) {
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5}; fma.rn.f32x2 x, x, y, z; "
+      "mov.b64 {%0, %1}, x;}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -103,15 +120,29 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float h_lo(uint32_t w) {
-  float f;
-  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(f) : "r"(w));
-  return f;
+// w less the fp16 in the low (high) half of h, exact where h is w rounded; s * f for a
+// bf16 s in the low half of its word and a power of two f; and s * 8 + c.  One mixed
+// instruction each, where widening first would take another.
+__device__ __forceinline__ float less_lo(float w, uint32_t h) {
+  float d;
+  asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, l, m, %2;}" : "=f"(d) : "r"(h), "f"(w));
+  return d;
 }
-__device__ __forceinline__ float h_hi(uint32_t w) {
-  float f;
-  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h;}" : "=f"(f) : "r"(w));
-  return f;
+__device__ __forceinline__ float less_hi(float w, uint32_t h) {
+  float d;
+  asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, h, m, %2;}" : "=f"(d) : "r"(h), "f"(w));
+  return d;
+}
+__device__ __forceinline__ float step_times(uint32_t s, float f) {
+  float d;
+  asm("{.reg .b16 l, h, x, y; mov.b32 {l, h}, %1; mov.b32 {x, y}, %2; fma.rn.f32.bf16 %0, l, y, 0f00000000;}"
+      : "=f"(d) : "r"(s), "r"(__float_as_uint(f)));
+  return d;
+}
+__device__ __forceinline__ float step8_plus(uint32_t s, float c) {
+  float d;
+  asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0x4100; fma.rn.f32.bf16 %0, l, m, %2;}" : "=f"(d) : "r"(s), "f"(c));
+  return d;
 }
 // 8x8 matrix of 16-bit entries, a row's pair 2c, 2c + 1 in lane (row, c): transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -310,7 +341,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
   float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
 #pragma unroll
   for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
-  float m_ref[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // of queries 2c, 2c + 1
+  float m_neg[2] = {INFINITY, INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // -reference of queries 2c, 2c + 1
   float l_run[2] = {0.0f, 0.0f};                            // of the same, this lane's keys
   float om[NG][2];                                          // sum of p (m + 8 s), the same
 #pragma unroll
@@ -382,7 +413,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
     float xm[2];
     uint32_t vmax = 0u;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) xm[e] = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
+    for (int e = 0; e < 2; ++e) xm[e] = fmaxf(max3(x[0][0][e], x[0][1][e], x[1][0][e]), x[1][1][e]);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -409,8 +440,8 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
         al[e] = 1.0f;
         if (mx > thr[e]) {
           const float mn = mx * c2[e];
-          al[e] = ex2(m_ref[e] - mn);                       // 0 the first time
-          m_ref[e] = mn;
+          al[e] = ex2(-m_neg[e] - mn);                      // 0 the first time
+          m_neg[e] = -mn;
           thr[e] = (mn + kD4Slack) / c2[e];
           l_run[e] *= al[e];
 #pragma unroll
@@ -427,12 +458,12 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[k][h][e] = ex2(fmaf(x[k][h][e], c2[e], -m_ref[e]));   // the weight p
-          l_run[e] += x[k][h][e];
-        }
+      for (int h = 0; h < 2; ++h) {                           // the weights p
+        fma2(x[k][h][0], x[k][h][1], c2[0], c2[1], m_neg[0], m_neg[1]);
+        x[k][h][0] = ex2(x[k][h][0]);
+        x[k][h][1] = ex2(x[k][h][1]);
+        add2(l_run[0], l_run[1], x[k][h][0], x[k][h][1]);
+      }
 
     // ---- out^T += V^T (p s)
 #pragma unroll
@@ -443,14 +474,14 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float s = bf_lo(vp[k][h][g]), m8 = fmaf(8.0f, s, bf_hi(vp[k][h][g])), sx = s * s_mul;
+          const float m8 = step8_plus(vp[k][h][g], bf_hi(vp[k][h][g])), sx = step_times(vp[k][h][g], s_mul);
           const float p0 = x[k][h][0], p1 = x[k][h][1];
           om[g][0] = fmaf(p0, m8, om[g][0]);
           om[g][1] = fmaf(p1, m8, om[g][1]);
           const float w0 = p0 * sx, w1 = p1 * sx;
           const uint32_t w = pack_h2(w0, w1);
           hi[k][h] = transpose8(w);
-          lo[k][h] = transpose8(pack_h2(w0 - h_lo(w), w1 - h_hi(w)));
+          lo[k][h] = transpose8(pack_h2(less_lo(w0, w), less_hi(w1, w)));
         }
       __syncwarp();
       uint32_t vw[2][2][2];
@@ -476,8 +507,8 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
           mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], hi[0][0], hi[0][1], d[0], d[1], d[2], d[3]);
           mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], hi[1][0], hi[1][1], d[0], d[1], d[2], d[3]);
           float(&acc)[4] = o[4 * g + 2 * wl + h];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] += d[j];
+          add2(acc[0], acc[1], d[0], d[1]);
+          add2(acc[2], acc[3], d[2], d[3]);
         }
     }
     __syncwarp();                                             // the stage is read
@@ -497,7 +528,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
       for (int g = 0; g < NG; ++g) om[g][e] += __shfl_xor_sync(kFullMask, om[g][e], sh);
     }
     if (r == 0) {
-      s_m[warp][2 * c + e] = m_ref[e];
+      s_m[warp][2 * c + e] = -m_neg[e];
       s_l[warp][2 * c + e] = l_run[e];
     }
 #pragma unroll
