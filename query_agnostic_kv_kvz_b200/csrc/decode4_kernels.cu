@@ -18,21 +18,27 @@
 // float32.
 //
 // fp16 operands: q is scaled by a power of two to a largest entry of 2^14
-// (bf16's 8 bits stay exact down to 2^-27 of it); a weight p s, scaled by a
+// (bf16's 8 bits stay exact down to 2^-31 of it); a weight p s, scaled by a
 // power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
 // for s), is the sum of two fp16 numbers, 22 bits.
 //
-// Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At that
-// rate an SM has to widen and multiply a row (both of K and V, all queries)
-// in 6 clocks, so the instructions per row bound it as much as HBM does.
+// Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
+// rate an SM would have to widen and multiply a row (both of K and V, all
+// queries) in 6 clocks.  What bounds it is issue: 64 heads of 32,768 rows at
+// d = 128, G = 5 (302 MB) take 77 us, 3.9 TB/s; the same loads without the
+// arithmetic take 55 us, the arithmetic without the loads 74.  A stage of 32
+// rows costs a warp 730 instructions, of which the 48 products hold the tensor
+// pipe for 31% of the time and the integer pipe is busy for 46%.
 //
-// One CTA of 8 warps takes an equal share of the blocks of all heads, whatever
+// One CTA of 8 warps takes an equal share of the work of all heads, whatever
 // the heads' lengths (a share may end one head and begin others).  A warp
 // brings its blocks in by bulk copy through a ring of its own, 32 rows a stage
-// (one copy where they share a page), and keeps a running (reference, sum, output) per query; the
-// warps merge in shared memory at the end of each head's part.  A head that
-// several CTAs read leaves one partial per CTA, which a second launch joins
-// in order: no atomics, and identical inputs give identical results.
+// (one copy where they share a page), and keeps a running (reference, sum,
+// output) per query; the warps merge in shared memory at the end of each
+// head's part.  A head that several CTAs read leaves one partial per CTA,
+// which a second launch joins in order: no atomics, and identical inputs give
+// identical results.  (One CTA of 16 warps per SM: 82.3 against 81 us, and
+// 31.9 against 24.3 at 96 uneven heads; 12 warps of 168 registers: 88.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -54,6 +60,12 @@ constexpr int kD4Warps = 8;
 constexpr int kD4Threads = kD4Warps * 32;
 constexpr int kD4Stages = 2;
 constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share is at least a stage per warp
+// What beginning another head costs a CTA (its queries, the ring's switch, the
+// join of the warps), counted as blocks: 64 heads of 32,768 rows (d = 128, G =
+// 5) took 80.5 us with 0, 80.0 with 8, 79.1 with 16, 77.0 with 40, 78.3 with
+// 72; 96 heads of very uneven lengths, 5,001 rows in the mean (d = 64, G = 8),
+// 24.0, 23.6, 22.2, 19.9 and 20.5.
+constexpr int kD4HeadCost = 40;
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
 
@@ -184,6 +196,11 @@ __device__ __forceinline__ uint4 load_16(const void* p) {
 
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t cap) {
   return c < 0 || c > cap ? 0 : (c + kC4Rows - 1) / kC4Rows;
+}
+// A head's weight in the shares: its blocks, behind kD4HeadCost more that stand for its beginning.
+__device__ __forceinline__ int64_t weight_of(int c, int64_t cap) {
+  const int64_t n = blocks_of(c, cap);
+  return n > 0 ? n + kD4HeadCost : 0;
 }
 
 // Inclusive scan over the CTA's threads; returns the sum.
@@ -591,14 +608,14 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   let_next_start();                                           // the merge may take its places as CTAs leave
   after_prior();
 
-  // ---- this CTA's share [u0, u1) of all heads' blocks: their number, then the head that holds block u0
+  // ---- this CTA's share [u0, u1) of all heads' weights: their sum, then the head that holds u0
   int64_t mine = 0;
   for (int64_t b = tid; b < p.B; b += kD4Threads) {
     const int n = load_int(p.counts + b);
     if (b < kD4Counts) s_cnt[b] = n;
-    mine += blocks_of(n, p.cap);
+    mine += weight_of(n, p.cap);
   }
-  int64_t inc;                                                // blocks of the threads up to this one
+  int64_t inc;                                                // weights of the threads up to this one
   int64_t total = cta_scan(mine, inc, s_red);
   int64_t quota = (total + kD4Workers - 1) / kD4Workers;
   quota = quota < kD4MinBlocks ? kD4MinBlocks : quota;
@@ -629,7 +646,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     int64_t carry = 0;
     for (int64_t b0 = 0; b0 < p.B && carry <= u0; b0 += kD4Threads) {
       const int64_t b = b0 + tid;
-      const int64_t n = b < p.B ? blocks_of(count_of(b), p.cap) : 0;
+      const int64_t n = b < p.B ? weight_of(count_of(b), p.cap) : 0;
       const int64_t all = cta_scan(n, inc, s_red);
       const int64_t start = carry + inc - n;
       if (u0 >= start && u0 < start + n) {
@@ -640,13 +657,18 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     }
   }
   __syncthreads();
-  int64_t start = s_find[1];                                  // of the part's head
+  int64_t start = s_find[1] + kD4HeadCost;                    // where the blocks of the part's head start
   auto part_of = [&](int64_t b, int64_t at) -> Part4 {
     const int count = count_of(b);
     const int64_t n = blocks_of(count, p.cap);
-    return Part4{static_cast<int>(b), count, static_cast<int>(u0 > at ? u0 - at : 0), static_cast<int>(u1 - at < n ? u1 - at : n)};
+    return Part4{static_cast<int>(b), count, static_cast<int>(u0 > at ? u0 - at : 0),
+                 static_cast<int>(u1 - at < n ? u1 - at : n)};
   };
   Part4 part = part_of(s_find[0], start);
+  if (part.a1 <= 0) {                                         // a share of a head's beginning alone
+    if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
 
   Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0};
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
@@ -656,10 +678,11 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     const int64_t n_blk = blocks_of(part.count, p.cap);
     if (tid == 0) {
       s_then.b = -1;
-      if (start + n_blk < u1) {                               // there is a next head: u1 <= total
+      const int64_t next = start + n_blk + kD4HeadCost;
+      if (next < u1) {                                        // there is a next head: u1 is at most the sum of weights
         int64_t nb = part.b;
         do ++nb; while (blocks_of(count_of(nb), p.cap) == 0);
-        s_then = part_of(nb, start + n_blk);
+        s_then = part_of(nb, next);
       }
     }
     __syncthreads();                                          // also: the warps' states of the last part are read
@@ -687,7 +710,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     if (part.a0 == 0 && past)                                 // this CTA begins the head, others go on with it
       cont = make_int4(part.b, static_cast<int>((start + n_blk - 1) / quota), 0, 0);
     if (s_then.b < 0) break;
-    start += n_blk;
+    start += n_blk + kD4HeadCost;
     part = s_then;
     __syncthreads();                                          // s_then is read
   }
