@@ -39,7 +39,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 // The blocks of all heads as one index space: head b's start at
 // block_base(b) = offsets[b] / 16 + SPARE * b, so heads of any lengths share
 // the grid evenly: a warp takes an equal run of blocks, finds the first one's
-// head by bisection and walks on from there.  A head of n rows has at most
+// head by search and walks on from there.  A head of n rows has at most
 // n / 16 + 1 blocks from its row 0 on (SPARE = 1), and a run of n rows that
 // begins inside one touches at most n / 16 + 2 (SPARE = 2).
 template <int SPARE>
@@ -60,10 +60,14 @@ struct BlockWalk {
     end = u + each < total ? u + each : total;
   }
   __device__ __forceinline__ int64_t head(const int64_t* offsets, int64_t B) const {
-    int64_t lo = 0, hi = B - 1;                               // largest b with block_base(b) <= u
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (block_base(offsets, mid) <= u) lo = mid; else hi = mid - 1;
+    int64_t lo = 0;                                           // largest b with block_base(b) <= u: 32 steps of the
+    for (int64_t n = B; n > 1;) {                             // range at a time (lane 0 stands for "at least lo")
+      const int lane = threadIdx.x & 31;
+      const int64_t step = (n + 31) >> 5, at = lane * step;
+      const unsigned below = __ballot_sync(kFullMask, lane == 0 || (at < n && block_base(offsets, lo + at) <= u));
+      const int64_t skip = (31 - __clz(below)) * step;
+      lo += skip;
+      n = n - skip < step ? n - skip : step;
     }
     return lo;
   }
