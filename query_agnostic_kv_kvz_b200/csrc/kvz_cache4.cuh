@@ -39,17 +39,23 @@ struct C4 {
   static constexpr int LPR = D / 8;                           // lanes that hold a row, 8 dims each
 };
 
-// Block blk of head b: its address, or null (and a report) for a page id
-// outside the pool.  The caller has checked blk against the table's width.
+// The page id of block blk of head b (the caller has checked blk against the
+// table's width), and the block's address there: null, and a report, for an
+// id outside the pool.
+__device__ __forceinline__ int32_t page_id(const Pages4& pg, int64_t b, uint32_t blk) {
+  return __ldg(pg.pages + b * pg.max_pages + page_of(pg, blk));
+}
 template <int D>
-__device__ __forceinline__ uint8_t* block_at(const Pages4& pg, int64_t b, uint32_t blk, int32_t* status) {
-  const uint32_t pi = page_of(pg, blk);
-  const int32_t id = __ldg(pg.pages + b * pg.max_pages + pi);
+__device__ __forceinline__ uint8_t* block_of(const Pages4& pg, int32_t id, uint32_t blk, int32_t* status) {
   if (id < 0 || id >= pg.n_pages) {
     report(status, KVZ_ERR_INVALID_ARG);
     return nullptr;
   }
-  return pg.cache + (static_cast<int64_t>(id) * pg.blocks + (blk - pi * pg.blocks)) * C4<D>::BLOCK;
+  return pg.cache + (static_cast<int64_t>(id) * pg.blocks + (blk - page_of(pg, blk) * pg.blocks)) * C4<D>::BLOCK;
+}
+template <int D>
+__device__ __forceinline__ uint8_t* block_at(const Pages4& pg, int64_t b, uint32_t blk, int32_t* status) {
+  return block_of<D>(pg, page_id(pg, b, blk), blk, status);
 }
 
 // x (the low or high bf16 of w) + y, rounded once: one full-rate instruction,
