@@ -19,9 +19,15 @@ namespace kvz {
 
 namespace {
 
-constexpr int kC4Threads = 256;
-constexpr int kCompactCtas = 2;                               // CTAs per SM of the largest grids: resident at once, and
-constexpr int kExpandCtas = 12;                               // four waves (measured: 2, 4, 6 and 3, 4, 8, 12, 24)
+// Small CTAs, since a warp's chain of loads is its time: 32 x 515 ragged
+// tokens appended (and read back) took 15.8, 14.2 and 16.3 us with 256, 128
+// and 64 threads; 32 heads of about 9,830 of 32,768 rows compacted (and read
+// back) 75.1, 74.5 and 74.3.
+constexpr int kC4Threads = 64, kAppendThreads = 128;
+constexpr int kQHeads = 2;                                    // query heads a thread turns by one set of angles
+constexpr int kCompactCtas = 512 / kC4Threads;                // CTAs per SM of the largest grids: resident at once, and
+constexpr int kExpandCtas = 3072 / kC4Threads;                // several waves (512 to 1,536 and 768 to 6,144 threads
+                                                              // were measured)
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -100,7 +106,7 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[2 * 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kC4Threads, 2)
+__global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
     compact_int4_kernel(const uint16_t* K, const uint16_t* V, int64_t B, int64_t n_c,
                         const int32_t* idx, const int32_t* counts,
                         const int64_t* offsets, Pages4 pg, int64_t cap, int32_t* status) {
@@ -396,12 +402,12 @@ __device__ __forceinline__ void turn_row(uint4& x, int lane, int l, const RotArg
 // single token is latency, and K, V and queries go to warps of their own; two
 // and four chains side by side in a warp were no faster on long prompts either.
 template <int D>
-__global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, uint32_t n_warps, uint32_t n_pairs,
+__global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(Append4Args a, uint32_t n_warps, uint32_t n_pairs,
                                                                  uint32_t kv_warps, uint32_t q_warps, int64_t cap) {
   using L = C4<D>;
   constexpr int PW = 16 / L::LPR;
   const int lane = threadIdx.x & 31, l = lane % L::LPR;
-  uint32_t w = (blockIdx.x * kC4Threads + threadIdx.x) >> 5;
+  uint32_t w = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);   // below 2^30; its threads may pass 2^32
   let_next_start();
   after_prior(a.k, a.v, a.q, a.rot.pos, a.rot.table, a.pg.cache, a.pg.pages, a.counts, a.n_new);
   const bool turning = a.rot.pos != nullptr;
@@ -473,43 +479,43 @@ __global__ void __launch_bounds__(kC4Threads) append_int4_kernel(Append4Args a, 
   }
   w -= 2 * kv_warps;
   if (w < q_warps) {
-    // a thread per 16 dims (whole pairs) of a token, all G rows of it by the same angles
+    // a thread per 16 dims (whole pairs) of a token in kQHeads heads, its values on the way before its angles (all
+    // heads in a thread: 15.9 us against 14.2 for 32 x 515 ragged tokens)
     constexpr uint32_t IT = D / 16;
-    const uint32_t f = w * 32 + lane, item = f % IT, bt = f / IT, T = static_cast<uint32_t>(a.T);
+    const uint32_t n_g = (static_cast<uint32_t>(a.G) + kQHeads - 1) / kQHeads, T = static_cast<uint32_t>(a.T);
+    const uint32_t item = lane % IT, rest = w * (32 / IT) + lane / IT, bt = rest / n_g;
+    const int g0 = static_cast<int>(rest - bt * n_g) * kQHeads;
     const uint32_t b = bt / T, t = bt - b * T;
     if (b >= a.B || (a.n_new != nullptr && static_cast<int32_t>(t) >= a.n_new[b])) return;
     const int rot = a.rot.rot, nrot = turning ? rot / 16 : 0;
     const bool turn = static_cast<int>(item) < nrot, il = a.rot.interleaved != 0;
     const int d0 = turn ? (il ? 16 * item : 8 * item) : (turning ? rot : 0) + 16 * (static_cast<int>(item) - nrot);
     const int d1 = turn && !il ? d0 + rot / 2 : d0 + 8;
+    const uint16_t* const q = a.q + b * a.q_sb + t * a.q_st;
+    uint4 v0[kQHeads], v1[kQHeads];
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i)
+      if (g0 + i < a.G) {
+        v0[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d0);
+        v1[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d1);
+      }
     float c[8], s[8];
     if (turning) {
       const int32_t p = a.rot.pos[b * a.rot.pos_sb + t];
       if (p < 0 || p >= a.rot.n_pos) return;                  // (reported with the head's keys)
       if (turn) load_angles(a.rot.table + static_cast<int64_t>(p) * rot, rot / 2, 8 * item, 0, c, s);
     }
-    const uint16_t* const q = a.q + b * a.q_sb + t * a.q_st;
-    // two heads in flight: 60 registers (four took 80 and 16.9 us against 15.9 for 32 x 515 ragged tokens, one 16.1)
-    for (int g0 = 0; g0 < a.G; g0 += 2) {
-      uint4 v0[2], v1[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (g0 + i < a.G) {
-          v0[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d0);
-          v1[i] = *reinterpret_cast<const uint4*>(q + (g0 + i) * a.q_sg + d1);
+    for (int i = 0; i < kQHeads; ++i)
+      if (g0 + i < a.G) {
+        if (turn) {
+          if (il) turn_adjacent(v0[i], v1[i], c, s);
+          else turn_halves(v0[i], v1[i], c, s);
         }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (g0 + i < a.G) {
-          if (turn) {
-            if (il) turn_adjacent(v0[i], v1[i], c, s);
-            else turn_halves(v0[i], v1[i], c, s);
-          }
-          uint16_t* const y = a.q_out + ((static_cast<int64_t>(b) * a.G + g0 + i) * T + t) * D;
-          *reinterpret_cast<uint4*>(y + d0) = v0[i];
-          *reinterpret_cast<uint4*>(y + d1) = v1[i];
-        }
-    }
+        uint16_t* const y = a.q_out + ((static_cast<int64_t>(b) * a.G + g0 + i) * T + t) * D;
+        *reinterpret_cast<uint4*>(y + d0) = v0[i];
+        *reinterpret_cast<uint4*>(y + d1) = v1[i];
+      }
     return;
   }
 }
@@ -547,10 +553,10 @@ cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream)
   const int64_t n_pairs = a.T / 2 + 1;                        // a run of T slots touches at most this many
   const int64_t n_warps = a.counts_out == nullptr ? 0 : a.B;
   const int64_t kv_warps = (a.B * n_pairs + pw - 1) / pw;
-  const int64_t q_warps = a.q == nullptr ? 0 : (a.B * a.T * (d / 16) + 31) / 32;
-  const int64_t grid = ((n_warps + 2 * kv_warps + q_warps) * 32 + kC4Threads - 1) / kC4Threads;
+  const int64_t q_warps = a.q == nullptr ? 0 : (a.B * a.T * ((a.G + kQHeads - 1) / kQHeads) * (d / 16) + 31) / 32;
+  const int64_t grid = ((n_warps + 2 * kv_warps + q_warps) * 32 + kAppendThreads - 1) / kAppendThreads;
   return launch_after(d == 128 ? append_int4_kernel<128> : append_int4_kernel<64>, dim3(static_cast<unsigned>(grid)),
-                      dim3(kC4Threads), 0, stream, 0, a, static_cast<uint32_t>(n_warps), static_cast<uint32_t>(n_pairs),
+                      dim3(kAppendThreads), 0, stream, 0, a, static_cast<uint32_t>(n_warps), static_cast<uint32_t>(n_pairs),
                       static_cast<uint32_t>(kv_warps), static_cast<uint32_t>(q_warps), table_rows(a.pg));
 }
 
