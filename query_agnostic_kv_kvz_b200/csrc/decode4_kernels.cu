@@ -720,8 +720,10 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
 // Few rows a head: latency counts, and the shares of the other kernel (a scan
 // of all counts, parts of two heads in a CTA, a second launch) cost more than
 // equal work gains.  Here a cluster of CTAs reads a head, rank j the j-th of
-// its equal parts, and joins its CTAs' states through distributed shared
-// memory, each CTA for a part of the dims.
+// its equal parts.  Every CTA sends its state to the cluster's CTAs, each of
+// which joins a part of the dims: four dims in the lanes of a warp, a lane per
+// CTA that sent them.  (Fetching the others' states took two round trips and a
+// barrier more, 2 us of 8.3 at 8 heads of 2,457 rows.)
 template <int D>
 __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4Args p) {
   using S = D4<D>;
@@ -730,12 +732,13 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   __shared__ int s_abort;
   __shared__ float s_m[kD4Warps][8], s_l[kD4Warps][8];
   __shared__ Part4 s_then;
-  __shared__ float s_cm[8], s_cl[8];                          // this CTA's reference and sum per query
-  __shared__ __align__(16) float s_co[8 * D];                 // and output
+  __shared__ float4 s_co[2 * D];                              // [C][8 D / 4 / C] outputs of the cluster's CTAs
+  __shared__ float2 s_cml[2 * D];                             // and (reference, sum) of their queries
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, G = p.G;
   const int64_t b = blockIdx.x / C;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA's shared memory is there
   let_next_start();
   if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
   if (tid == 0) s_abort = 0;
@@ -749,6 +752,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     } else if (rank == 0 && tid == 0) {
       report(p.status, KVZ_ERR_INVALID_ARG);
     }
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
   // parts in whole stages, so that only the head's last block can stand alone
@@ -761,34 +765,34 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   __syncthreads();                                            // the barriers are initialised
   const bool ok = read_part<D>(p, Part4{static_cast<int>(b), count, a0, a1}, &s_then, ring, &s_abort, s_o, s_m, s_l);
   const bool failed = __syncthreads_or(!ok);
-  for (int e4 = tid; e4 < G * D / 4; e4 += kD4Threads) {
-    const int g = 4 * e4 / D;
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const int n4 = G * D / 4;
+  if (tid < n4) {                                             // n4 <= 2 D <= kD4Threads
     float M, Ls;
-    const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
-    reinterpret_cast<float4*>(s_co)[e4] = acc;
-    if ((4 * e4) % D == 0) {
-      s_cm[g] = M;
-      s_cl[g] = failed ? NAN : Ls;                            // a part that was not read spoils its head, not others
-    }
+    const float4 acc = join_warps<D>(tid, s_o, s_m, s_l, M, Ls);
+    if (failed) Ls = NAN;                                     // a part that was not read spoils its head, not others
+    const int to = tid & (C - 1), at = rank * (2 * D / C) + tid / C;
+    cluster.map_shared_rank(s_co, to)[at] = acc;
+    cluster.map_shared_rank(s_cml, to)[at] = make_float2(M, Ls);
   }
   cluster.sync();
-  for (int e4 = rank * kD4Threads + tid; e4 < G * D / 4; e4 += C * kD4Threads) {
-    const int g = 4 * e4 / D;
-    float M = -INFINITY, Ls = 0.0f;
-    for (int j = 0; j < C; ++j) M = fmaxf(M, cluster.map_shared_rank(s_cm, j)[g]);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int j = 0; j < C; ++j) {
-      const float mj = cluster.map_shared_rank(s_cm, j)[g], lj = cluster.map_shared_rank(s_cl, j)[g];
-      const float wgt = mj == -INFINITY && lj == 0.0f ? 0.0f : exp2f(mj - M);
-      const float4 v = reinterpret_cast<const float4*>(cluster.map_shared_rank(s_co, j))[e4];
-      Ls = fmaf(lj, wgt, Ls);
-      acc.x = fmaf(v.x, wgt, acc.x), acc.y = fmaf(v.y, wgt, acc.y);
-      acc.z = fmaf(v.z, wgt, acc.z), acc.w = fmaf(v.w, wgt, acc.w);
-    }
-    reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + g] = M + log2f(Ls);
+  const int j = tid & (C - 1), e4 = rank + (tid & ~(C - 1));  // C lanes of a warp join output e4
+  const float2 ml = e4 < n4 ? s_cml[j * (2 * D / C) + tid / C] : make_float2(-INFINITY, 0.0f);
+  float4 acc = e4 < n4 ? s_co[j * (2 * D / C) + tid / C] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float M = ml.x;
+  for (int o = 1; o < C; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  const float w = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : exp2f(ml.x - M);   // 0: a CTA without rows
+  float Ls = ml.y * w;
+  acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
+  for (int o = 1; o < C; o <<= 1) {
+    Ls += __shfl_xor_sync(kFullMask, Ls, o);
+    acc.x += __shfl_xor_sync(kFullMask, acc.x, o), acc.y += __shfl_xor_sync(kFullMask, acc.y, o);
+    acc.z += __shfl_xor_sync(kFullMask, acc.z, o), acc.w += __shfl_xor_sync(kFullMask, acc.w, o);
   }
-  cluster.sync();                                             // the others have read this CTA's state
+  if (e4 < n4 && j == 0) {
+    reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = M + log2f(Ls);
+  }
 }
 
 // The heads that CTA blockIdx.x began and others went on with: their partials
@@ -877,6 +881,10 @@ cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
   if (C > 0) {
     cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(D4<D>::SMEM);
     if (e != cudaSuccess) return e;
+    if (C > 8) {
+      e = cudaFuncSetAttribute(decode_int4_cluster_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
     return launch_after(decode_int4_cluster_kernel<D>, dim3(static_cast<unsigned>(a.B * C)), dim3(kD4Threads),
                         D4<D>::SMEM, stream, C, a);
   }
