@@ -877,16 +877,15 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
 
 template <int D>
 cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
-  const int C = decode4_cluster(a.B, a.cap);
-  if (C > 0) {
-    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(D4<D>::SMEM);
+  const Decode4Form form = decode4_form(a.B, a.cap);
+  if (form.cluster > 0) {
+    constexpr int kAlone = 115 * 1024;                        // of an SM's 228 KB: one CTA
+    static_assert(D4<D>::SMEM <= kAlone, "");
+    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(kAlone);
+    if (e == cudaSuccess && form.cluster > 8) e = wide_clusters_once<decode_int4_cluster_kernel<D>>();
     if (e != cudaSuccess) return e;
-    if (C > 8) {
-      e = cudaFuncSetAttribute(decode_int4_cluster_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-    }
-    return launch_after(decode_int4_cluster_kernel<D>, dim3(static_cast<unsigned>(a.B * C)), dim3(kD4Threads),
-                        D4<D>::SMEM, stream, C, a);
+    return launch_after(decode_int4_cluster_kernel<D>, dim3(static_cast<unsigned>(a.B * form.cluster)), dim3(kD4Threads),
+                        form.alone ? kAlone : D4<D>::SMEM, stream, form.cluster, a);
   }
   cudaError_t e = smem_limit_once<decode_int4_kernel<D>>(D4<D>::SMEM);
   if (e != cudaSuccess) return e;

@@ -164,7 +164,7 @@ kvz_status kvz_append_int4(const void* k, int64_t k_sb, int64_t k_st, const void
 
 size_t kvz_decode_int4_workspace_size(int64_t B, int G, int64_t rows, int d) {
   if (B < 1 || B > 65535 || G < 1 || G > kvz::kDecGMax || (d != 64 && d != 128) || rows < 1) return 0;
-  if (kvz::decode4_cluster(B, rows) > 0) return 0;
+  if (kvz::decode4_form(B, rows).cluster > 0) return 0;
   const size_t w = kvz::kD4Workers;
   return up256(w * sizeof(int4)) + up256(2 * w * 8 * sizeof(float2)) + up256(2 * w * G * d * sizeof(float));
 }

@@ -9,20 +9,28 @@
 
 namespace kvz {
 
-// Raise a kernel's dynamic shared-memory limit once per device (the launch
-// paths call this before every launch; the attribute call itself is a host
-// round trip worth skipping).  `bytes` is a constant of the kernel.
-template <auto Kernel>
-cudaError_t smem_limit_once(int bytes) {
+// Set a kernel's attribute once per device (the launch paths call this before
+// every launch; the attribute call itself is a host round trip worth
+// skipping).  `value` is a constant of the kernel.
+template <auto Kernel, cudaFuncAttribute Attr>
+cudaError_t attribute_once(int value) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t(1) << dev) : 0;
   if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(Kernel, Attr, value);
   if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+template <auto Kernel>
+cudaError_t smem_limit_once(int bytes) {                      // dynamic shared memory
+  return attribute_once<Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize>(bytes);
+}
+template <auto Kernel>
+cudaError_t wide_clusters_once() {                            // clusters of more than 8 CTAs
+  return attribute_once<Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
 }
 
 // Pass 1 (row log-sum-exp) arguments.  Rows i in [i_begin, i_end) are
@@ -240,17 +248,29 @@ struct Dec4Args {
   int32_t* status;
 };
 // The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
-// table holds `cap` rows, or 0 for shares of equal work.  A cluster costs less
-// to start and join (us for 64 heads of 1,000 rows 10 against 17; of 8,000
-// rows 26 against 32; one head of 4,000 rows 9.1 against 10.3), shares cost
-// less where few CTAs, or a head far longer than the rest, would carry all (one
-// head of 8,000 rows 10.6 against 12.4, of 32,000 rows 14 against 30).  Lengths
-// are on the device, so the table's width stands for the longest head.
-inline int decode4_cluster(int64_t B, int64_t cap) {
+// table holds `cap` rows, or 0 for shares of equal work; `alone`: each on an SM
+// of its own.  us at d = 128, G = 4, clusters against shares:
+//   1 head     2,000 rows 6.1 : 8.7    8,000 rows  8.1 :  9.1   16,000 rows 10.9 : 9.7
+//   6 heads               6.2 : 9.2                8.5 : 11.7               11.3 : 13.3
+//   12 heads              6.7 : 11.3              11.3 : 12.7               16.9 : 16.2
+//   20 heads              8.1 : 11.6   4,000 rows 11.0 : 12.7    6,000 rows 13.9 : 13.9
+//   32 heads             10.8 : 12.7   8,000 rows 18.5 : 18.7   12,000 rows 23.6 : 22.5
+//   96 heads             15.2 : 18.4   4,000 rows 24.0 : 24.2    6,000 rows 33.1 : 31.0
+// So clusters take the shorter heads.  Lengths are on the device, so the
+// table's width stands for the longest.  Few heads: the most CTAs up to 96
+// that have an SM each (more clusters do not fit the GPU's GPCs side by side:
+// 16 heads by 8 CTAs 8.7 us packed, 12.1 alone, by 4 alone 8.0 at 2,000 rows).
+// Else the most up to 256 (37 heads by 8 CTAs, 296 in all, 15.0; by 4, 11.0).
+struct Decode4Form {
+  int cluster;
+  bool alone;
+};
+inline Decode4Form decode4_form(int64_t B, int64_t cap) {
+  for (int c = 16; c >= 4; c /= 2)
+    if (c * B <= 96) return Decode4Form{cap <= c * 1280 ? c : 0, true};
   int c = 1;
-  while (c < 8 && 2 * c * B <= kD4Workers) c *= 2;            // fill the GPU once, at most a portable cluster
-  const int64_t rows = 2 * c * B >= kD4Workers ? 2048 : 1024; // a CTA's rows at most (half or more of the GPU, or less)
-  return cap <= c * rows ? c : 0;
+  while (c < 8 && 2 * c * B <= 256) c *= 2;
+  return Decode4Form{cap <= c * (c <= 4 && c * B >= 192 ? 2048 : 1280) ? c : 0, false};
 }
 cudaError_t launch_decode_int4(int d, const Dec4Args& a, cudaStream_t stream);
 

@@ -67,6 +67,12 @@ def filled(counts, d, page, seed, scale=1.0):
     return cache, pages, n, k, v
 
 
+def wide(pages, page, rows=40000):
+    """The page table with unused entries up to `rows` rows: attention then takes shares of equal work."""
+    more = torch.full((pages.shape[0], max(0, rows // page - pages.shape[1])), -1, dtype=torch.int32, device="cuda")
+    return torch.cat([pages, more], 1)
+
+
 def offsets_of(lengths):
     return torch.tensor([0] + list(np.cumsum(lengths)), dtype=torch.int64, device="cuda")
 
@@ -283,7 +289,21 @@ def check_decode(q, cache, pages, counts, page, scale, **kw):
 ])
 def test_decode(G, counts, page, d):
     cache, pages, n, _, _ = filled(counts, d, page, len(counts) + G)
-    check_decode(rand((len(counts), G, d), G), cache, pages, n, page, d ** -0.5)
+    q, B = rand((len(counts), G, d), G), len(counts)
+    out, lse2 = check_decode(q, cache, pages, n, page, d ** -0.5)
+    more = wide(pages, page)
+    assert kvz.kvz_decode_int4_workspace_size(B, G, more.shape[1] * page, d) > 0
+    out2, lse22 = check_decode(q, cache, more, n, page, d ** -0.5)
+    assert torch.equal(torch.isneginf(lse2), torch.isneginf(lse22))
+
+
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 7), (128, 8), (64, 1)])
+@pytest.mark.parametrize("B", [1, 7, 12, 13, 24, 25, 33, 64, 65, 129])
+def test_decode_by_clusters_of_every_size(B, d, G):
+    counts = [0 if b % 5 == 3 else (b * 97 + 350) % 701 for b in range(B)]
+    cache, pages, n, _, _ = filled(counts, d, 32, B)
+    assert kvz.kvz_decode_int4_workspace_size(B, G, pages.shape[1] * 32, d) == 0
+    check_decode(rand((B, G, d), B), cache, pages, n, 32, d ** -0.5)
 
 
 def test_decode_one_long_head():
@@ -369,6 +389,7 @@ def test_decode_shared_pages():
 
 def test_decode_is_deterministic_and_leaves_inputs():
     cache, pages, n, _, _ = filled([5000, 40, 9000, 123], 128, 64, 23)
+    pages = wide(pages, 64)
     q, c0 = rand((4, 8, 128), 24), cache.clone()
     need = kvz.kvz_decode_int4_workspace_size(4, 8, pages.shape[1] * 64, 128)
     assert need > 0
@@ -577,6 +598,7 @@ def test_decoding_in_graphs_that_share_a_workspace():
     n0 = torch.tensor(counts, dtype=torch.int32, device="cuda")
     kvz.kvz_append_int4(k0, v0, cache, pages, zero, page, n_new=n0)
     other = filled([33, 12000, 1], d, page, 42)
+    pages, other = wide(pages, page), (other[0], wide(other[1], page), other[2])
     need = kvz.kvz_decode_int4_workspace_size(B, G, pages.shape[1] * page, d)
     assert need == kvz.kvz_decode_int4_workspace_size(B, G, other[1].shape[1] * page, d) > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -608,6 +630,80 @@ def test_decoding_in_graphs_that_share_a_workspace():
         ref, _ = check_decode(q_out.view(B, G, d), cache, pages, cnt, page, d ** -0.5)
         assert torch.equal(got, ref)
         assert torch.equal(out2, kvz.kvz_decode_int4(q_out.view(B, G, d), other[0], other[1], other[2], page)[0])
+
+
+def test_calls_that_follow_each_other_at_once():
+    # a kernel may start while the one before it ends: the same steps with and without a wait after each call
+    d, page, B, G, T = 128, 32, 5, 4, 40
+    t = table(d, 200)
+    k, v, q = rand((T, B, 1, d), 50), rand((T, B, 1, d), 51), rand((T, B, G, 1, d), 52)
+    runs = []
+    for wait in (True, False):
+        cache, pages = pool([T + 60] * B, d, page, 4)
+        pages = torch.stack([pages, pages])               # copies, so that the two forms alternate
+        n = torch.tensor([0, 1, 17, 31, 60], dtype=torch.int32, device="cuda")
+        kvz.kvz_append_int4(rand((B, 60, d), 53), rand((B, 60, d), 54), cache, pages[0],
+                            torch.zeros_like(n), page, n_new=n)
+        tabs = (pages[0], wide(pages[1], page))
+        torch.cuda.synchronize()
+        outs = []
+        for i in range(T):
+            n, qr = kvz.kvz_append_int4(k[i], v[i], cache, tabs[0], n, page, positions=n[:, None], table=t, q=q[i])
+            if wait:
+                torch.cuda.synchronize()
+            qi = kvz.kvz_rotary(qr, n[:, None], t, inverse=True)
+            if wait:
+                torch.cuda.synchronize()
+            o, l2 = kvz.kvz_decode_int4(qr.view(B, G, d), cache, tabs[i % 2], n, page)
+            if wait:
+                torch.cuda.synchronize()
+            outs += [qr, qi, o, l2]
+        K, V = kvz.kvz_expand_int4(cache, tabs[0], n, offsets_of([T + c for c in (0, 1, 17, 31, 60)]), page,
+                                   out_rows=5 * T + 109)
+        torch.cuda.synchronize()
+        runs.append(outs + [n, K, V, cache])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    # the same cache read by two streams, each with its own workspace, and a third call over another cache
+    cache, pages, n, _, _ = filled([3000, 12, 9000], 128, 64, 60)
+    pages = wide(pages, 64)
+    q = [rand((3, 4, 128), 61 + i) for i in range(2)]
+    ref = [kvz.kvz_decode_int4(x, cache, pages, n, 64) for x in q]
+    need = kvz.kvz_decode_int4_workspace_size(3, 4, pages.shape[1] * 64, 128)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in q]
+    out = [[torch.empty_like(r) for r in rs] for rs in ref]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                kvz.kvz_decode_int4(q[i], cache, pages, n, 64, out=out[i][0], lse2=out[i][1], workspace=ws[i])
+    torch.cuda.synchronize()
+    for a, b in zip(ref, out):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_every_step():
+    # a group for every normal bf16 as its range: the step's reciprocal is division's for each
+    top = (torch.arange(128, 255 * 128, dtype=torch.int32) << 16).view(torch.float32)
+    g = torch.Generator().manual_seed(70)
+    x = torch.rand((top.numel(), 64), generator=g)
+    x[:, 0], x[:, 1] = 0.0, 1.0
+    x = (x.double() * top[:, None].double()).to(torch.bfloat16)
+    rows = x.view(-1, 128).cuda()
+    n = rows.shape[0]
+    cache, pages = pool([n], 128, 64, 7)
+    counts = torch.tensor([n], dtype=torch.int32, device="cuda")
+    idx = torch.arange(n, dtype=torch.int32, device="cuda")
+    other = rows.flip(0).contiguous()
+    kvz.kvz_compact_int4(rows[None], other[None], idx, counts, offsets_of([n]), cache, pages, 64)
+    K, V = kvz.kvz_expand_int4(cache, pages, counts, offsets_of([n]), 64, out_rows=n)
+    for src, got in ((rows, K), (other, V)):
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(src))))
+        np.testing.assert_array_equal(bits(got), ref)
 
 
 def test_whole_path_from_scores_to_answers():
