@@ -686,6 +686,26 @@ def test_two_streams_at_once():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_compact_uses_the_counted_indexes_only():
+    # offsets may leave a head more room than its rows; what lies there is no index
+    B, n_c, d, page, room = 3, 300, 64, 32, 200
+    K, V = rand((B, n_c, d), 71), rand((B, n_c, d), 72)
+    counts = [17, 0, 160]
+    idx = torch.full((B * room,), -5, dtype=torch.int32, device="cuda")
+    for b, c in enumerate(counts):
+        idx[b * room:b * room + c] = torch.arange(c, dtype=torch.int32, device="cuda") + b
+    n = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    cache, pages = pool(counts, d, page, 8)
+    st = new_status()
+    kvz.kvz_compact_int4(K, V, idx, n, offsets_of([room] * B), cache, pages, page, status=st)
+    got = kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), page, out_rows=sum(counts))
+    assert st.item() == 0
+    for src, out in ((K, got[0]), (V, got[1])):
+        rows = torch.cat([src[b, b:b + c] for b, c in enumerate(counts)])
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(rows))))
+        np.testing.assert_array_equal(bits(out), ref)
+
+
 def test_every_step():
     # a group for every normal bf16 as its range: the step's reciprocal is division's for each
     top = (torch.arange(128, 255 * 128, dtype=torch.int32) << 16).view(torch.float32)
