@@ -471,6 +471,52 @@ def test_bad_pages_are_reported():
         assert st.item() == 1 and bool((K[72:] == 5).all()) and not bool((K[40:72] == 5).any())
 
 
+def test_bad_counts_and_pages_in_shares_of_equal_work():
+    # heads that several CTAs read, with one left out before them, and a bad page in the middle of one
+    counts, d, page = [9000, 50, 12000, 0, 700], 64, 32
+    cache, pages, n, _, _ = filled(counts, d, page, 34)
+    pages = wide(pages, page)
+    q = rand((5, 3, d), 35)
+    good = kvz.kvz_decode_int4(q, cache, pages, n, page)
+    for bad in (-1, pages.shape[1] * page + 1, -2 ** 31):
+        m, st = n.clone(), new_status()
+        m[0] = bad
+        out = torch.full((5, 3, d), 5.0, device="cuda")
+        kvz.kvz_decode_int4(q, cache, pages, m, page, out=out, status=st)
+        assert st.item() == 1 and bool((out[0] == 5).all())
+        assert torch.allclose(out[1:], good[0][1:], atol=1e-5)
+    for bad in (-1, cache.shape[0], -2 ** 31):
+        p, st = pages.clone(), new_status()
+        p[2, 200] = bad
+        out, _ = kvz.kvz_decode_int4(q, cache, p, n, page, status=st)
+        assert st.item() == 1
+        keep = torch.tensor([0, 1, 3, 4], device="cuda")
+        assert torch.equal(out[keep], good[0][keep])
+
+
+def test_tensors_on_the_host_are_refused():
+    counts, d, page = [40, 3], 64, 16
+    cache, pages, n, k, v = filled(counts, d, page, 36)
+    q, c0 = rand((2, 2, d), 37), cache.clone()
+    pos = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    calls = {
+        kvz.kvz_decode_int4: dict(q=q, cache=cache, pages=pages, counts=n, page_size=page, status=new_status()),
+        kvz.kvz_append_int4: dict(k=k[:, :1], v=v[:, :1], cache=cache, pages=pages, counts=n, page_size=page,
+                                  positions=pos, table=table(64, 8), n_new=torch.ones_like(n), status=new_status()),
+        kvz.kvz_expand_int4: dict(cache=cache, pages=pages, counts=n, offsets=offsets_of(counts), page_size=page,
+                                  out_rows=43, status=new_status()),
+        kvz.kvz_compact_int4: dict(K=k, V=v, idx=torch.zeros(43, dtype=torch.int32, device="cuda"), counts=n,
+                                   offsets=offsets_of(counts), cache=cache, pages=pages, page_size=page),
+        kvz.kvz_rotary: dict(x=k[:, :1], positions=pos, table=table(64, 8), status=new_status()),
+    }
+    for f, kw in calls.items():
+        for name, t in kw.items():
+            if isinstance(t, torch.Tensor):
+                with pytest.raises(ValueError):
+                    f(**{**kw, name: t.cpu()})
+    assert torch.equal(cache, c0)
+
+
 def test_append_refusals_on_the_device():
     d, page = 64, 16
     cache, pages, n, _, _ = filled([30, 30, 30, 30], d, page, 34)
