@@ -306,6 +306,15 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
   const int r = lane >> 2, c = lane & 3;
   const int G = p.G;
   const int n = part.stages(warp), all = n + then->stages(warp);
+  // the queries are on their way before the first stages are looked up and issued
+  uint4 v[NG][2];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v[g][u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < G) v[g][u] = load_16(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
+    }
   while (q.issued < kD4Stages && q.issued < all) q.issue_next(p, part, then, n, warp, lane, q.issued);   // warp-uniform
 
   // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
@@ -314,14 +323,11 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
   uint32_t qb[S::KS][2];
   float qs[NG][2], c2[2];
   {
-    uint4 v[NG][2];
     uint32_t ef = 0;                                        // largest exponent field of the query
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        v[g][u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < G) v[g][u] = load_16(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
         const uint32_t w[4] = {v[g][u].x, v[g][u].y, v[g][u].z, v[g][u].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) ef = max(ef, max((w[k] >> 23) & 0xFFu, (w[k] >> 7) & 0xFFu));
