@@ -224,15 +224,17 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t& inc, int64_t* s_
   return all;
 }
 
-// Blocks [a0, a1) of head b's `count` rows; none: b < 0.  Its 32-row stages go
-// to the CTA's warps in turn.
+// Blocks [a0, a1) of head b's `count` rows; none: b < 0.  Of their 32-row
+// stages every 2^spread-th is the CTA's; those go to its warps in turn.
 struct Part4 {
   int b, count, a0, a1;
-  __device__ __forceinline__ int stages(int warp) const {
-    const int n = b < 0 ? 0 : (a1 - a0 + 1) / 2;
+  __device__ __forceinline__ int stages(int warp, int spread) const {
+    const int n = b < 0 ? 0 : (a1 - a0 + (2 << spread) - 1) >> (1 + spread);
     return n > warp ? (n - warp + kD4Warps - 1) / kD4Warps : 0;
   }
-  __device__ __forceinline__ int block(int warp, int i) const { return a0 + 2 * (warp + kD4Warps * i); }
+  __device__ __forceinline__ int block(int warp, int i, int spread) const {
+    return a0 + ((2 * (warp + kD4Warps * i)) << spread);
+  }
 };
 
 // A warp's ring of stages, kept full across the parts that its CTA reads one
@@ -245,31 +247,40 @@ struct Ring4 {
   uint32_t used;                                              // stages taken
   int issued;                                                 // of the current part's (and then the next one's) stages
   int at0, at1;                                               // pool blocks of stage lane, lane + 32, ...
+  bool placed;                                                // the first 32 of them are there from the start
 
-  __device__ __forceinline__ void look_up(const Dec4Args& p, const Part4& t, int warp, int i) {
-    if (i >= t.stages(warp)) return;
-    const uint32_t blk = static_cast<uint32_t>(t.block(warp, i));
-    const uint32_t pi0 = page_of(p.pg, blk);
-    const uint32_t pi1 = static_cast<int>(blk) + 1 < t.a1 ? page_of(p.pg, blk + 1) : pi0;
-    const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(t.b) * p.pg.max_pages;
-    int id0 = load_int(row_pages + pi0), id1 = load_int(row_pages + pi1);
-    if (id0 < 0 || id0 >= p.pg.n_pages || id1 < 0 || id1 >= p.pg.n_pages) {
+  // The page ids of a stage's two blocks, blk and blk + 1, of head b (the second as the first from block `end` on).
+  static __device__ __forceinline__ int2 ids(const Dec4Args& p, int b, int blk, int end) {
+    const int32_t* const row_pages = p.pg.pages + static_cast<int64_t>(b) * p.pg.max_pages;
+    const uint32_t pi0 = page_of(p.pg, static_cast<uint32_t>(blk));
+    const uint32_t pi1 = blk + 1 < end ? page_of(p.pg, static_cast<uint32_t>(blk) + 1) : pi0;
+    return make_int2(load_int(row_pages + pi0), load_int(row_pages + pi1));
+  }
+  __device__ __forceinline__ void place(const Dec4Args& p, int2 id, int blk) {
+    if (id.x < 0 || id.x >= p.pg.n_pages || id.y < 0 || id.y >= p.pg.n_pages) {
       report(p.status, KVZ_ERR_INVALID_ARG);                  // page 0 stands in, so the read stays inside
-      id0 = id0 < 0 || id0 >= p.pg.n_pages ? 0 : id0;
-      id1 = id1 < 0 || id1 >= p.pg.n_pages ? 0 : id1;
+      id.x = id.x < 0 || id.x >= p.pg.n_pages ? 0 : id.x;
+      id.y = id.y < 0 || id.y >= p.pg.n_pages ? 0 : id.y;
     }
-    at0 = id0 * static_cast<int>(p.pg.blocks) + static_cast<int>(blk - pi0 * p.pg.blocks);
-    at1 = pi1 == pi0 ? at0 + 1 : id1 * static_cast<int>(p.pg.blocks);
+    const uint32_t pi0 = page_of(p.pg, static_cast<uint32_t>(blk)), pi1 = page_of(p.pg, static_cast<uint32_t>(blk) + 1);
+    at0 = id.x * static_cast<int>(p.pg.blocks) + blk - static_cast<int>(pi0 * p.pg.blocks);
+    at1 = pi1 == pi0 ? at0 + 1 : id.y * static_cast<int>(p.pg.blocks);
+  }
+  __device__ __forceinline__ void look_up(const Dec4Args& p, const Part4& t, int warp, int i, int spread) {
+    if (i >= t.stages(warp, spread)) return;
+    const int blk = t.block(warp, i, spread);
+    place(p, ids(p, t.b, blk, t.a1), blk);
   }
   // Issue the copies of stage i of part t, `ahead` stages past the one now due.
-  __device__ __forceinline__ void issue(const Dec4Args& p, const Part4& t, int warp, int lane, int i, int ahead) {
+  __device__ __forceinline__ void issue(const Dec4Args& p, const Part4& t, int warp, int lane, int i, int ahead,
+                                        int spread) {
     using L = C4<D>;
-    if ((i & 31) == 0) look_up(p, t, warp, i + lane);
+    if ((i & 31) == 0 && !(placed && i == 0)) look_up(p, t, warp, i + lane, spread);
     const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
     if (lane == 0) {
       const uint32_t st = (used + static_cast<uint32_t>(ahead)) % kD4Stages;
       uint8_t* const dst = ring + st * D4<D>::STAGE;
-      const bool two = t.block(warp, i) + 1 < t.a1, joined = two && from1 == from0 + 1;
+      const bool two = t.block(warp, i, spread) + 1 < t.a1, joined = two && from1 == from0 + 1;
       mbar_arrive_expect_tx(&bar[st], two ? 2 * L::BLOCK : L::BLOCK);
       bulk_load(dst, p.pg.cache + static_cast<int64_t>(from0) * L::BLOCK, joined ? 2 * L::BLOCK : L::BLOCK, &bar[st]);
       if (two && !joined)
@@ -279,9 +290,9 @@ struct Ring4 {
   // The next stage that is not under way: of part t (n stages), then of the part after it (all - n), which lies in
   // shared memory since it is looked at so rarely.
   __device__ __forceinline__ void issue_next(const Dec4Args& p, const Part4& t, const Part4* then, int n, int warp,
-                                             int lane, int ahead) {
-    if (issued < n) issue(p, t, warp, lane, issued, ahead);
-    else issue(p, *then, warp, lane, issued - n, ahead);
+                                             int lane, int ahead, int spread) {
+    if (issued < n) issue(p, t, warp, lane, issued, ahead, spread);
+    else issue(p, *then, warp, lane, issued - n, ahead, spread);
     ++issued;
   }
   // Let the copies under way land (bounded), behind `taken` stages done with, before the CTA leaves early.
@@ -292,30 +303,39 @@ struct Ring4 {
   }
 };
 
+// A lane's share of head b's queries: query lane / 4, 16 dims of each group.
+template <int D>
+struct Query4 {
+  uint4 v[D / 64][2];
+  __device__ __forceinline__ void load(const Dec4Args& p, int64_t b) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        v[g][u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < p.G) v[g][u] = load_16(p.q + (b * p.G + r) * D + 64 * g + 16 * c + 8 * u);
+      }
+  }
+};
+
 // One part of a head, read by the CTA's warps 32 rows at a time; each leaves its
 // reference, sum and output per query in shared memory.  `then` (in shared
 // memory) is the part that the CTA reads next.  False in a warp whose wait
 // expired.
 template <int D>
-__device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, const Part4* then, Ring4<D>& q,
-                                          volatile int* abort_flag, float* s_o, float (*s_m)[8], float (*s_l)[8]) {
+__device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& query, const Part4& part,
+                                          const Part4* then, Ring4<D>& q,
+                                          volatile int* abort_flag, float* s_o, float (*s_m)[8], float (*s_l)[8],
+                                          int spread) {
   using L = C4<D>;
   using S = D4<D>;
   constexpr int NG = L::NG;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
-  const int G = p.G;
-  const int n = part.stages(warp), all = n + then->stages(warp);
-  // the queries are on their way before the first stages are looked up and issued
-  uint4 v[NG][2];
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      v[g][u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < G) v[g][u] = load_16(p.q + (static_cast<int64_t>(part.b) * G + r) * D + 64 * g + 16 * c + 8 * u);
-    }
-  while (q.issued < kD4Stages && q.issued < all) q.issue_next(p, part, then, n, warp, lane, q.issued);   // warp-uniform
+  const auto& v = query.v;
+  const int n = part.stages(warp, spread), all = n + then->stages(warp, spread);
+  while (q.issued < kD4Stages && q.issued < all) q.issue_next(p, part, then, n, warp, lane, q.issued, spread);   // warp-uniform
 
   // Q^T fragments (columns = queries; those >= G are zero), scaled by a power of
   // two to a largest exponent of 14; lane (r, c) loads query r and then works on
@@ -380,7 +400,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
       break;
     }
     const uint8_t* stage = q.ring + st * S::STAGE;
-    const int blk0 = part.block(warp, i);
+    const int blk0 = part.block(warp, i, spread);
     // rows of the stage that count: the head may end inside it, and this CTA's share after its first block (what
     // lies past them, in the page or left in the stage, has no influence)
     const int rows = min(part.count - blk0 * kC4Rows, (part.a1 - blk0) * kC4Rows);
@@ -536,7 +556,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Part4& part, 
     }
     __syncwarp();                                             // the stage is read
     ++q.used;
-    if (q.issued < all) q.issue_next(p, part, then, n, warp, lane, kD4Stages - 1);
+    if (q.issued < all) q.issue_next(p, part, then, n, warp, lane, kD4Stages - 1, spread);
   }
   if (ok) q.issued -= n;                                      // the rest belongs to the next part
 
@@ -676,11 +696,13 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     return;
   }
 
-  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0};
+  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, false};
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
   int4 cont = make_int4(-1, 0, 0, 0);
 
   for (;;) {
+    Query4<D> query;                                          // on its way before the first stages are issued
+    query.load(p, part.b);
     const int64_t n_blk = blocks_of(part.count, p.cap);
     if (tid == 0) {
       s_then.b = -1;
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       }
     }
     __syncthreads();                                          // also: the warps' states of the last part are read
-    const bool ok = read_part<D>(p, part, &s_then, ring, &s_abort, s_o, s_m, s_l);
+    const bool ok = read_part<D>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, 0);
     if (__syncthreads_or(!ok)) {                              // uniform: the output of this share is not written
       if (ok) ring.drain(lane, 0);
       if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -725,12 +747,12 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
 
 // Few rows a head: latency counts, and the shares of the other kernel (a scan
 // of all counts, parts of two heads in a CTA, a second launch) cost more than
-// equal work gains.  Here a cluster of CTAs reads a head, rank j the j-th of
-// its equal parts.  Every CTA sends its state to the cluster's CTAs, each of
+// equal work gains.  Here the CTAs of a cluster read a head, its 32-row stages
+// in turn over all their warps.  Every CTA sends its state to the cluster's CTAs, each of
 // which joins a part of the dims: four dims in the lanes of a warp, a lane per
-// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 7.2 us in a
-// chain of calls, of which the first 1.9 pass before the first rows are there
-// (count, page, rows: one load after another) and 1.5 in the join; 8.3 when
+// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 6.9 us in a
+// chain of calls, of which the first 1.6 pass before the first rows are there
+// (count and page, then rows) and 1.5 in the join; a microsecond more when
 // every CTA fetched the others' states, two round trips and a barrier more.
 template <int D>
 __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4Args p) {
@@ -752,7 +774,13 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   if (tid == 0) s_abort = 0;
   fence_mbar_init();
   after_prior();
+  // stages in turn over the cluster's CTAs and their warps, so that where a warp's stages are does not depend on the
+  // head's rows: their pages are looked up beside the count
+  const int lane = tid & 31, blk = 2 * (rank + C * (warp + kD4Warps * lane)), tab = static_cast<int>(p.cap / kC4Rows);
+  const int2 early = blk < tab ? Ring4<D>::ids(p, static_cast<int>(b), blk, tab) : make_int2(0, 0);
   const int count = load_int(p.counts + b);                   // the same in all CTAs of the cluster
+  Query4<D> query;
+  query.load(p, b);
   if (count <= 0 || count > p.cap) {
     if (rank == 0 && count == 0) {
       for (int e = tid; e < G * D; e += kD4Threads) p.out[b * G * D + e] = 0.0f;
@@ -763,15 +791,14 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
-  // parts in whole stages, so that only the head's last block can stand alone
-  const int n_blk = (count + kC4Rows - 1) / kC4Rows, n_st = (n_blk + 1) / 2;
-  const int a0 = 2 * static_cast<int>(static_cast<int64_t>(n_st) * rank / C);
-  const int a1 = min(2 * static_cast<int>(static_cast<int64_t>(n_st) * (rank + 1) / C), n_blk);
+  const Part4 part{static_cast<int>(b), count, 2 * rank, (count + kC4Rows - 1) / kC4Rows};
+  const int spread = 31 - __clz(C);                           // (C is a power of two)
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
-  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0};
+  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, true};
+  if (blk < part.a1) ring.place(p, make_int2(early.x, blk + 1 < part.a1 ? early.y : early.x), blk);
   if (tid == 0) s_then.b = -1;
   __syncthreads();                                            // the barriers are initialised
-  const bool ok = read_part<D>(p, Part4{static_cast<int>(b), count, a0, a1}, &s_then, ring, &s_abort, s_o, s_m, s_l);
+  const bool ok = read_part<D>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, spread);
   const bool failed = __syncthreads_or(!ok);
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   const int n4 = G * D / 4;
@@ -798,7 +825,8 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     acc.z += __shfl_xor_sync(kFullMask, acc.z, o), acc.w += __shfl_xor_sync(kFullMask, acc.w, o);
   }
   if (e4 < n4 && j == 0) {
-    reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
+    const float inv = 1.0f / Ls;
+    reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = M + log2f(Ls);
   }
 }
