@@ -745,6 +745,24 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
   if (tid == 0) p.cont[blockIdx.x] = cont;
 }
 
+// Write to the same shared variable of CTA `rank` of the cluster; its barrier,
+// likewise, counts the bytes as they land.
+__device__ __forceinline__ uint32_t mapa(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void send(uint32_t at, const float4& v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void send(uint32_t at, const float2& v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+               "f"(v.x), "f"(v.y), "r"(bar)
+               : "memory");
+}
+
 // Few rows a head: latency counts, and the shares of the other kernel (a scan
 // of all counts, parts of two heads in a CTA, a second launch) cost more than
 // equal work gains.  Here the CTAs of a cluster read a head, its 32-row stages
@@ -764,15 +782,21 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   __shared__ Part4 s_then;
   __shared__ float4 s_co[2 * D];                              // [C][8 D / 4 / C] outputs of the cluster's CTAs
   __shared__ float2 s_cml[2 * D];                             // and (reference, sum) of their queries
+  __shared__ uint64_t s_all;                                  // counts both as they land
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, G = p.G;
   const int64_t b = blockIdx.x / C;
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA's shared memory is there
+  const int n4 = G * D / 4;
   let_next_start();
   if (tid < kD4Warps * kD4Stages) mbar_init(&full[tid], 1);
-  if (tid == 0) s_abort = 0;
+  if (tid == 0) {
+    s_abort = 0;
+    mbar_init(&s_all, 1);
+    mbar_arrive_expect_tx(&s_all, static_cast<uint32_t>(n4 * (sizeof(float4) + sizeof(float2))));
+  }
   fence_mbar_init();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // this CTA may be sent to
   after_prior();
   // stages in turn over the cluster's CTAs and their warps, so that where a warp's stages are does not depend on the
   // head's rows: their pages are looked up beside the count
@@ -788,7 +812,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     } else if (rank == 0 && tid == 0) {
       report(p.status, KVZ_ERR_INVALID_ARG);
     }
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;
   }
   const Part4 part{static_cast<int>(b), count, 2 * rank, (count + kC4Rows - 1) / kC4Rows};
@@ -800,17 +824,18 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   __syncthreads();                                            // the barriers are initialised
   const bool ok = read_part<D>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, spread);
   const bool failed = __syncthreads_or(!ok);
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  const int n4 = G * D / 4;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < n4) {                                             // n4 <= 2 D <= kD4Threads
     float M, Ls;
     const float4 acc = join_warps<D>(tid, s_o, s_m, s_l, M, Ls);
     if (failed) Ls = NAN;                                     // a part that was not read spoils its head, not others
     const int to = tid & (C - 1), at = rank * (2 * D / C) + tid / C;
-    cluster.map_shared_rank(s_co, to)[at] = acc;
-    cluster.map_shared_rank(s_cml, to)[at] = make_float2(M, Ls);
+    const uint32_t bar = mapa(&s_all, to);
+    send(mapa(s_co + at, to), acc, bar);
+    send(mapa(s_cml + at, to), make_float2(M, Ls), bar);
   }
-  cluster.sync();
+  // (past the limit of the others' own waits: each sends in any case)
+  if (!mbar_wait_for(&s_all, 0, 2 * kWaitLimitNs)) report(p.status, KVZ_ERR_TIMEOUT);
   const int j = tid & (C - 1), e4 = rank + (tid & ~(C - 1));  // C lanes of a warp join output e4
   const float2 ml = e4 < n4 ? s_cml[j * (2 * D / C) + tid / C] : make_float2(-INFINITY, 0.0f);
   float4 acc = e4 < n4 ? s_co[j * (2 * D / C) + tid / C] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
