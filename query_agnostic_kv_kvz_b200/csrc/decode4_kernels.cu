@@ -25,10 +25,10 @@
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
 // rate an SM would have to widen and multiply a row (both of K and V, all
 // queries) in 6 clocks.  What bounds it is issue: 64 heads of 32,768 rows at
-// d = 128, G = 5 (302 MB) take 77 us, 3.9 TB/s; the same loads without the
+// d = 128, G = 5 (302 MB) take 76 us, 4.0 TB/s; the same loads without the
 // arithmetic take 55 us, the arithmetic without the loads 74.  A stage of 32
-// rows costs a warp 730 instructions, of which the 48 products hold the tensor
-// pipe for 31% of the time and the integer pipe is busy for 46%.
+// rows costs a warp 680 instructions: issue slots are 58% busy, the integer
+// pipe 42%, the tensor pipe (48 products) 34%.
 //
 // One CTA of 8 warps takes an equal share of the work of all heads, whatever
 // the heads' lengths (a share may end one head and begin others).  A warp
@@ -768,9 +768,9 @@ __device__ __forceinline__ void send(uint32_t at, const float2& v, uint32_t bar)
 // equal work gains.  Here the CTAs of a cluster read a head, its 32-row stages
 // in turn over all their warps.  Every CTA sends its state to the cluster's CTAs, each of
 // which joins a part of the dims: four dims in the lanes of a warp, a lane per
-// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 6.9 us in a
+// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 6.7 us in a
 // chain of calls, of which the first 1.6 pass before the first rows are there
-// (count and page, then rows) and 1.5 in the join; a microsecond more when
+// (count and page, then rows) and 1.2 in the join; a microsecond more when
 // every CTA fetched the others' states, two round trips and a barrier more.
 template <int D>
 __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4Args p) {

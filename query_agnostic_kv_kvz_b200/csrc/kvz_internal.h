@@ -250,17 +250,18 @@ struct Dec4Args {
 // The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
 // table holds `cap` rows, or 0 for shares of equal work; `alone`: each on an SM
 // of its own.  us at d = 128, G = 4, clusters against shares:
-//   1 head     2,000 rows 6.1 : 8.7    8,000 rows  8.1 :  9.1   16,000 rows 10.9 : 9.7
-//   6 heads               6.2 : 9.2                8.5 : 11.7               11.3 : 13.3
-//   12 heads              6.7 : 11.3              11.3 : 12.7               16.9 : 16.2
-//   20 heads              8.1 : 11.6   4,000 rows 11.0 : 12.7    6,000 rows 13.9 : 13.9
-//   32 heads             10.8 : 12.7   8,000 rows 18.5 : 18.7   12,000 rows 23.6 : 22.5
-//   96 heads             15.2 : 18.4   4,000 rows 24.0 : 24.2    6,000 rows 33.1 : 31.0
+//   1 head     2,000 rows 5.3 : 8.4    8,000 rows  7.5 :  8.7   16,000 rows 10.5 : 9.4
+//   6 heads               5.6 : 9.0                7.8 : 11.4               10.8 : 12.9
+//   12 heads              6.1 : 10.9              10.7 : 12.5               16.9 : 15.7
+//   20 heads              7.5 : 11.5   4,000 rows 10.6 : 12.5    6,000 rows 13.7 : 13.6
+//   32 heads              9.8 : 12.5   8,000 rows 16.9 : 18.2   12,000 rows 21.7 : 22.0
+//   96 heads             14.8 : 17.8   4,000 rows 23.8 : 23.5    6,000 rows 32.7 : 30.5
 // So clusters take the shorter heads.  Lengths are on the device, so the
 // table's width stands for the longest.  Few heads: the most CTAs up to 96
 // that have an SM each (more clusters do not fit the GPU's GPCs side by side:
 // 16 heads by 8 CTAs 8.7 us packed, 12.1 alone, by 4 alone 8.0 at 2,000 rows).
 // Else the most up to 256 (37 heads by 8 CTAs, 296 in all, 15.0; by 4, 11.0).
+// CTAs of 16 warps, which fill an SM: 7.1 against 6.7 for 8 heads of 2,457 rows.
 struct Decode4Form {
   int cluster;
   bool alone;
