@@ -7,7 +7,7 @@
 // chain of dependent loads (head, page, index, row) behind a launch.  At d =
 // 128, in chains of calls: 311,051 of 32 x 32,768 rows compacted in 38.9 us
 // (5.3 TB/s) and expanded in 37.4 us (5.5 TB/s); 8 heads of 2,457 rows 5.4 and
-// 5.6 us; 32 ragged prompts, 8,716 tokens with 4 query heads each, appended in
+// 4.7 us; 32 ragged prompts, 8,716 tokens with 4 query heads each, appended in
 // 9.1 us (2.6 TB/s); one token for 128 heads in 2.2 us.
 #include <cuda_runtime.h>
 
@@ -30,6 +30,13 @@ namespace {
 // back) 75.1, 74.5 and 74.3.
 constexpr int kC4Threads = 64, kAppendThreads = 128;
 constexpr int kQHeads = 2;                                    // query heads a thread turns by one set of angles
+// Blocks up to which the rows read back go by two warps a block, one for K and
+// one for V: where a warp has one block, its instructions are its time (8 heads
+// of 2,457 rows 4.7 us against 5.6); where it has several, looking them up
+// twice costs more (64 uneven heads, 567,000 rows, 35.8 against 33.8).
+// Compaction, whose warps look up each row's index too, gains nothing (6.0
+// against 5.4).
+constexpr int64_t kExpandSplit = 2368;
 constexpr int kCompactCtas = 512 / kC4Threads;                // CTAs per SM of the largest grids: resident at once, and
 constexpr int kExpandCtas = 3072 / kC4Threads;                // several waves (512 to 1,536 and 768 to 6,144 threads
                                                               // were measured)
@@ -49,11 +56,11 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // The blocks of all heads as one index space: head b's start at
 // block_base(b) = offsets[b] / 16 + SPARE * b, so heads of any lengths share
-// the grid evenly: a warp takes an equal run of blocks, finds the first one's
+// the grid evenly: a warp (SPLIT: two) takes an equal run of blocks, finds the first one's
 // head by search and walks on from there.  A head of n rows has at most
 // n / 16 + 1 blocks from its row 0 on (SPARE = 1), and a run of n rows that
 // begins inside one touches at most n / 16 + 2 (SPARE = 2).
-template <int SPARE>
+template <int SPARE, bool SPLIT>
 struct BlockWalk {
   int64_t u, end;                                             // this warp's run of units
   int64_t b, base, next, o;                                   // head, its first unit, the next head's, offsets[b]
@@ -64,8 +71,8 @@ struct BlockWalk {
   }
   __device__ __forceinline__ void run(const int64_t* offsets, int64_t B) {
     const int64_t total = block_base(offsets, B);
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> 5;
-    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / 32);
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> (SPLIT ? 6 : 5);
+    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / (SPLIT ? 64 : 32));
     const int64_t each = (total + n_warps - 1) / n_warps;
     u = warp * each;
     end = u + each < total ? u + each : total;
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   let_next_start();
   after_prior(K, V, idx, counts, offsets, pg.cache, pg.pages);
-  BlockWalk<1> h;
+  BlockWalk<1, false> h;
   h.run(offsets, B);
   if (h.u >= h.end) return;                                   // warp-uniform, as is all that follows per block
   int64_t o1 = 0;
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
 
 // Rows first[b] .. counts[b] - 1 as bf16 rows offsets[b], offsets[b] + 1, ...
 // A value is one fused bf16 multiply-add, s * code + m rounded once.
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kC4Threads)
     expand_int4_kernel(Pages4 pg, const int32_t* counts, const int32_t* first,
                        const int64_t* offsets, int64_t B, int64_t cap, uint16_t* K_out,
@@ -256,7 +263,8 @@ __global__ void __launch_bounds__(kC4Threads)
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   let_next_start();
   after_prior(pg.cache, pg.pages, counts, first, offsets, K_out, V_out);
-  BlockWalk<2> h;
+  const bool do_k = !SPLIT || (threadIdx.x & 32) == 0, do_v = !SPLIT || !do_k;   // warp-uniform
+  BlockWalk<2, SPLIT> h;
   h.run(offsets, B);
   if (h.u >= h.end) return;
   auto enter = [&](int64_t b) {
@@ -308,8 +316,11 @@ __global__ void __launch_bounds__(kC4Threads)
     if (p != nullptr) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        load_words<2 * NG>(p + (r + 8 * k) * (D / 2) + c * (8 * NG), kw[k]);
-        load_words<NG>(p + L::KS_OFF + (r + 8 * k) * (4 * NG), ks[k]);
+        if (do_k) {
+          load_words<2 * NG>(p + (r + 8 * k) * (D / 2) + c * (8 * NG), kw[k]);
+          load_words<NG>(p + L::KS_OFF + (r + 8 * k) * (4 * NG), ks[k]);
+        }
+        if (!do_v) continue;
         // V: lane (r, c) takes r' = r of the pairs c and c + 4, rows 2c + 8k and 2c + 8k + 1
         load_words<2 * NG>(p + L::V_OFF + (c + 4 * k) * D + r * (8 * NG), vw[k]);
         load_words<2 * NG>(p + L::VS_OFF + (2 * c + 8 * k) * (4 * NG), vs[k]);
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(kC4Threads)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int row = r + 8 * k;
-      if (row >= lo && row < hi) {
+      if (do_k && row >= lo && row < hi) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const uint32_t s2 = __byte_perm(ks[k][g], 0u, 0x1010), m2 = __byte_perm(ks[k][g], 0u, 0x3232);
@@ -336,6 +347,7 @@ __global__ void __launch_bounds__(kC4Threads)
           put32(K_out + (out + row) * D + 64 * g + 16 * c, y);
         }
       }
+      if (!do_v) continue;
       const int even = 2 * c + 8 * k;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -547,9 +559,13 @@ cudaError_t launch_expand_int4(const Pages4& pg, const int32_t* counts, const in
                                int64_t B, int d, void* K_out, void* V_out, int64_t n_rows, int32_t* status,
                                cudaStream_t stream) {
   uint16_t *k = static_cast<uint16_t*>(K_out), *v = static_cast<uint16_t*>(V_out);
-  const unsigned grid = grid_for(n_rows / kC4Rows + 2 * B, kExpandCtas);
-  return launch_after(d == 128 ? expand_int4_kernel<128> : expand_int4_kernel<64>, dim3(grid), dim3(kC4Threads), 0, stream, 0,
-                      pg, counts, first, offsets, B, table_rows(pg), k, v, n_rows, status);
+  const int64_t units = n_rows / kC4Rows + 2 * B;
+  const bool split = units <= kExpandSplit;
+  const unsigned grid = grid_for(split ? 2 * units : units, kExpandCtas);
+  const auto kernel = split ? (d == 128 ? expand_int4_kernel<128, true> : expand_int4_kernel<64, true>)
+                            : (d == 128 ? expand_int4_kernel<128, false> : expand_int4_kernel<64, false>);
+  return launch_after(kernel, dim3(grid), dim3(kC4Threads), 0, stream, 0, pg, counts, first, offsets, B, table_rows(pg), k, v,
+                      n_rows, status);
 }
 
 cudaError_t launch_append_int4(int d, const Append4Args& a, cudaStream_t stream) {

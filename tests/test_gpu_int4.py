@@ -257,6 +257,20 @@ def test_expand_part():
     assert none[0].shape == (0, 128)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_expand_of_many_rows(d):
+    # so many blocks that a warp takes K and V of several, in heads of very different lengths
+    counts = [17, 0, 30011, 1, 9000, 64]
+    cache, pages, n, k, v = filled(counts, d, 48, 9)
+    st = new_status()
+    got = kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), 48, out_rows=sum(counts), status=st)
+    assert st.item() == 0
+    for src, out in ((k, got[0]), (v, got[1])):
+        rows = torch.cat([src[b, :c] for b, c in enumerate(counts)])
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(rows))))
+        np.testing.assert_array_equal(bits(out), ref)
+
+
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
