@@ -80,7 +80,8 @@ def build_fast(force: bool = False, verbose: bool = False) -> bool:
            "-DKVZ_TORCH_VERSION=\"%s\"" % torch.__version__,
            "-I" + os.path.join(t, "include"), "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-I" + INCLUDE, FAST_SRC,
-           "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+           "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd))
     try:

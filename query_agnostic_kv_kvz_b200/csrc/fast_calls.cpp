@@ -14,12 +14,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
+#include <optional>
 
 #include "kvz.h"
 
@@ -88,8 +90,10 @@ struct Args {
   }
   bool current() const { return ok && dev >= 0 && c10::cuda::current_device() == dev; }
   cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
+  // (through the dispatcher a call with two outputs takes 0.5 us more, 5.3 against 4.8)
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+    return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)),
+                                             std::nullopt));
   }
 
  private:
