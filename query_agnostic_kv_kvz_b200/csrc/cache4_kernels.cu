@@ -37,9 +37,8 @@ constexpr int kQHeads = 2;                                    // query heads a t
 // Compaction, whose warps look up each row's index too, gains nothing (6.0
 // against 5.4).
 constexpr int64_t kExpandSplit = 2368;
-constexpr int kCompactCtas = 512 / kC4Threads;                // CTAs per SM of the largest grids: resident at once, and
-constexpr int kExpandCtas = 3072 / kC4Threads;                // several waves (512 to 1,536 and 768 to 6,144 threads
-                                                              // were measured)
+constexpr int kCompactCtas = 8;                               // CTAs per SM of the largest grids: resident at once, and
+constexpr int kExpandCtas = 48;                               // several waves (8 to 24 and 12 to 96 were measured)
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
