@@ -341,6 +341,38 @@ def test_decode_many_heads_and_a_long_one():
     check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
 
 
+def test_the_most_heads():
+    # 65,535 heads of 0 to 16 rows: every call numbers them, and both forms of attention read them
+    B, d, page = 65535, 64, 16
+    n = (torch.arange(B, device="cuda", dtype=torch.int32) * 5) % 17
+    cache = torch.full((B, page * 72), 255, dtype=torch.uint8, device="cuda")
+    pages = torch.randperm(B, generator=torch.Generator().manual_seed(1))[:, None].int().cuda()
+    k, v, q = rand((B, 16, d), 91), rand((B, 16, d), 92), rand((B, 1, d), 93)
+    st = new_status()
+    got, _ = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros_like(n), page, n_new=n, status=st)
+    assert torch.equal(got, n)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), n.long().cumsum(0)])
+    rows = int(off[-1])
+    K, V = kvz.kvz_expand_int4(cache, pages, n, off, page, out_rows=rows, status=st)
+    live = torch.arange(16, device="cuda")[None] < n[:, None]
+    for src, out in ((k[live], K), (v[live], V)):
+        pick = torch.cat([torch.arange(500), torch.arange(rows - 500, rows)]).cuda()
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(src[pick]))))
+        np.testing.assert_array_equal(bits(out[pick]), ref)
+    again = torch.full_like(cache, 255)
+    idx = torch.arange(16, device="cuda", dtype=torch.int32)[None].expand(B, 16)[live]
+    kvz.kvz_compact_int4(k, v, idx, n, off, again, pages, page, status=st)
+    assert torch.equal(again, cache)
+    a = kvz.kvz_decode_int4(q, cache, pages, n, page, status=st)
+    b = kvz.kvz_decode_int4(q, cache, wide(pages, page, 2080), n, page, status=st)
+    assert kvz.kvz_decode_int4_workspace_size(B, 1, 2080, d) > 0 and st.item() == 0
+    for x, y in zip(a, b):
+        assert torch.allclose(x, y, atol=1e-5)
+    pick = torch.tensor([0, 1, 2, 3, 30000, B - 2, B - 1], device="cuda")
+    ref, _ = check_decode(q[pick], cache, pages[pick], n[pick], page, d ** -0.5)
+    assert torch.allclose(a[0][pick], ref, atol=1e-5)
+
+
 def test_decode_all_empty():
     cache, pages, n, _, _ = filled([0, 0, 0], 128, 16, 13)
     check_decode(rand((3, 4, 128), 3), cache, pages, n, 16, 0.1)
