@@ -454,7 +454,8 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /*                                                                          */
 /* kvz_compact_int4: for p < counts[b], row p of head b becomes row          */
 /*   idx[offsets[b] + p] of K, V [B][n_c][d] bf16 (idx, counts, offsets as   */
-/*   kvz_select writes them).  Other rows of the pages keep their bytes.     */
+/*   kvz_select writes them, or a run of B heads of theirs: offsets[0] need  */
+/*   not be 0).  Other rows of the pages keep their bytes.                   */
 /* kvz_append_int4: row counts[b] + t of head b becomes k[b][t], v[b][t], t <  */
 /*   n_new[b] (n_new NULL: T rows each; k[b][t] = k + b*k_sb + t*k_st, v and */
 /*   q[b][g][t] alike; strides in elements, multiples of 8).  With positions, */
@@ -466,7 +467,7 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /* kvz_expand_int4: rows first[b] (NULL: 0) .. counts[b] - 1 of head b, as   */
 /*   bf16(s * code + m), to rows offsets[b], offsets[b] + 1, ... of K_out,   */
 /*   V_out [n_rows][d].  offsets [B + 1] must ascend and leave each head its */
-/*   rows: the form kvz_decode and kvz_compact use.                          */
+/*   rows, from any row on: the form kvz_decode and kvz_compact use.         */
 /* kvz_decode_int4: kvz_decode over the 4-bit cache: q [B][G][d] bf16, out   */
 /*   [B][G][d] fp32, lse2 [B][G] fp32 (optional); a head without rows gives  */
 /*   out = 0, lse2 = -inf.  1 <= G <= 8.  Workspace:                         */

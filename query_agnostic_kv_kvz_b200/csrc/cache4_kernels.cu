@@ -54,22 +54,23 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 }
 
 // The blocks of all heads as one index space: head b's start at
-// block_base(b) = offsets[b] / 16 + SPARE * b, so heads of any lengths share
-// the grid evenly: a warp (SPLIT: two) takes an equal run of blocks, finds the first one's
+// block_base(b) = offsets[b] / 16 - offsets[0] / 16 + SPARE * b (the offsets
+// may start anywhere: one layer's heads among a stack's, rows kept in front),
+// so heads of any lengths share the grid evenly: a warp (SPLIT: two) takes an equal run of blocks, finds the first one's
 // head by search and walks on from there.  A head of n rows has at most
 // n / 16 + 1 blocks from its row 0 on (SPARE = 1), and a run of n rows that
 // begins inside one touches at most n / 16 + 2 (SPARE = 2).
 template <int SPARE, bool SPLIT>
 struct BlockWalk {
   int64_t u, end;                                             // this warp's run of units
+  int64_t o0;                                                 // offsets[0] / 16
   int64_t b, base, next, o;                                   // head, its first unit, the next head's, offsets[b]
   int32_t n, f;                                               // rows [f, n) of the head count (none for a bad head)
 
-  static __device__ __forceinline__ int64_t block_base(const int64_t* offsets, int64_t b) {
-    return (offsets[b] >> 4) + SPARE * b;
-  }
+  __device__ __forceinline__ int64_t base_of(int64_t o, int64_t b) const { return (o >> 4) - o0 + SPARE * b; }
   __device__ __forceinline__ void run(const int64_t* offsets, int64_t B) {
-    const int64_t total = block_base(offsets, B);
+    o0 = offsets[0] >> 4;
+    const int64_t total = base_of(offsets[B], B);
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> (SPLIT ? 6 : 5);
     const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / (SPLIT ? 64 : 32));
     const int64_t each = (total + n_warps - 1) / n_warps;
@@ -77,11 +78,11 @@ struct BlockWalk {
     end = u + each < total ? u + each : total;
   }
   __device__ __forceinline__ int64_t head(const int64_t* offsets, int64_t B) const {
-    int64_t lo = 0;                                           // largest b with block_base(b) <= u: 32 steps of the
+    int64_t lo = 0;                                           // largest b whose base is at most u: 32 steps of the
     for (int64_t n = B; n > 1;) {                             // range at a time (lane 0 stands for "at least lo")
       const int lane = threadIdx.x & 31;
       const int64_t step = (n + 31) >> 5, at = lane * step;
-      const unsigned below = __ballot_sync(kFullMask, lane == 0 || (at < n && block_base(offsets, lo + at) <= u));
+      const unsigned below = __ballot_sync(kFullMask, lane == 0 || (at < n && base_of(offsets[lo + at], lo + at) <= u));
       const int64_t skip = (31 - __clz(below)) * step;
       lo += skip;
       n = n - skip < step ? n - skip : step;
@@ -135,8 +136,8 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
     h.b = b;
     h.o = offsets[b];
     o1 = offsets[b + 1];
-    h.base = (h.o >> 4) + b;
-    h.next = (o1 >> 4) + b + 1;
+    h.base = h.base_of(h.o, b);
+    h.next = h.base_of(o1, b + 1);
     h.n = counts[b];
     fresh = true;
   };
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
     const uint32_t q = static_cast<uint32_t>(u - h.base);
     const int32_t id = p0 >= 0 && p0 < cap ? page_id(pg, h.b, q) : -1;
     settle();
-    if (p0 >= h.n) return;
+    if (p0 < 0 || p0 >= h.n) return;                          // (below 0: offsets that do not ascend)
     rows = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);
     int32_t from[2];
 #pragma unroll
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(kC4Threads)
     h.b = b;
     h.o = offsets[b];
     const int64_t o1 = offsets[b + 1];
-    h.base = (h.o >> 4) + 2 * b;
-    h.next = (o1 >> 4) + 2 * b + 2;
+    h.base = h.base_of(h.o, b);
+    h.next = h.base_of(o1, b + 1);
     h.n = counts[b];
     h.f = first == nullptr ? 0 : first[b];
     if (h.f < 0 || h.n < h.f || h.n > cap || h.n - h.f > o1 - h.o || h.o < 0 || h.o + (h.n - h.f) > n_rows) {
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kC4Threads)
     if (u >= h.end) return;
     while (u >= h.next && h.b + 1 < B) enter(h.b + 1);
     const int64_t q = (h.f >> 4) + u - h.base, p0 = q * kC4Rows;
-    if (p0 >= h.n) return;
+    if (q < 0 || p0 >= h.n) return;                           // (below 0: offsets that do not ascend)
     blk = block_at<D>(pg, h.b, static_cast<uint32_t>(q), status);
     from = static_cast<int>(h.f > p0 ? h.f - p0 : 0);
     to = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);

@@ -271,6 +271,38 @@ def test_expand_of_many_rows(d):
         np.testing.assert_array_equal(bits(out), ref)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("start", [5, 16, 256, 1000])
+@pytest.mark.parametrize("counts,page", [([100, 0, 37], 16), ([0, 100, 17, 1], 64), ([5000, 3, 40000], 48)])
+def test_offsets_that_start_behind_other_rows(counts, page, start, d):
+    # one layer's heads in the outputs of a stack: compaction takes its run of idx, expansion leaves the rows in front
+    cache, pages, n, k, v = filled(counts, d, page, start)
+    off = offsets_of(counts) + start
+    rows = start + sum(counts) + 3
+    K = torch.full((rows, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    V, st = K.clone(), new_status()
+    kvz.kvz_expand_int4(cache, pages, n, off, page, K_out=K, V_out=V, status=st)
+    assert st.item() == 0
+    want = kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), page, out_rows=sum(counts))
+    for out, ref in ((K, want[0]), (V, want[1])):
+        assert torch.equal(out[start:-3], ref)
+        assert bool((out[:start] == 3).all()) and bool((out[-3:] == 3).all())
+    first = n // 2
+    part = n - first
+    off_part = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), part.long().cumsum(0)]) + start
+    got = kvz.kvz_expand_int4(cache, pages, n, off_part, page, first=first, out_rows=rows, status=st)
+    at, o = 0, start
+    for c, m in zip(counts, part.tolist()):
+        for x, y in zip(want, got):
+            assert torch.equal(x[at + c - m:at + c], y[o:o + m])
+        at, o = at + c, o + m
+    other = torch.full_like(cache, 255)
+    idx = torch.full((rows,), -7, dtype=torch.int32, device="cuda")         # what lies in front is another head's
+    idx[start:start + sum(counts)] = torch.cat([torch.arange(c, dtype=torch.int32, device="cuda") for c in counts])
+    kvz.kvz_compact_int4(k, v, idx, n, off, other, pages, page, status=st)
+    assert st.item() == 0 and torch.equal(other, cache)
+
+
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
