@@ -54,28 +54,33 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 }
 
 // The blocks of all heads as one index space: head b's start at
-// block_base(b) = offsets[b] / 16 - offsets[0] / 16 + SPARE * b (the offsets
-// may start anywhere: one layer's heads among a stack's, rows kept in front),
-// so heads of any lengths share the grid evenly: a warp (SPLIT: two) takes an equal run of blocks, finds the first one's
-// head by search and walks on from there.  A head of n rows has at most
+// base_of(offsets[b], b) = offsets[b] / 16 + SPARE * b and the first one's at
+// its own (the offsets may start anywhere: one layer's heads among a stack's,
+// rows kept in front), so heads of any lengths share the grid evenly: a warp
+// (SPLIT: two) takes an equal run of blocks, finds the first one's head by
+// search and walks on from there.  A head of n rows has at most
 // n / 16 + 1 blocks from its row 0 on (SPARE = 1), and a run of n rows that
-// begins inside one touches at most n / 16 + 2 (SPARE = 2).
+// begins inside one touches at most n / 16 + 2 (SPARE = 2).  Offsets may leave
+// a head more room than its rows, any amount of it: a warp that comes to the
+// end of a head's rows goes on at the next head's first unit in one step.
 template <int SPARE, bool SPLIT>
 struct BlockWalk {
-  int64_t u, end;                                             // this warp's run of units
-  int64_t o0;                                                 // offsets[0] / 16
+  int64_t u, end;                                             // the next unit to look up, the end of this warp's run
   int64_t b, base, next, o;                                   // head, its first unit, the next head's, offsets[b]
   int32_t n, f;                                               // rows [f, n) of the head count (none for a bad head)
 
-  __device__ __forceinline__ int64_t base_of(int64_t o, int64_t b) const { return (o >> 4) - o0 + SPARE * b; }
+  static __device__ __forceinline__ int64_t base_of(int64_t o, int64_t b) { return (o >> 4) + SPARE * b; }
   __device__ __forceinline__ void run(const int64_t* offsets, int64_t B) {
-    o0 = offsets[0] >> 4;
-    const int64_t total = base_of(offsets[B], B);
+    const int64_t at0 = base_of(offsets[0], 0), at1 = base_of(offsets[B], B);
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kC4Threads + threadIdx.x) >> (SPLIT ? 6 : 5);
     const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kC4Threads / (SPLIT ? 64 : 32));
-    const int64_t each = (total + n_warps - 1) / n_warps;
-    u = warp * each;
-    end = u + each < total ? u + each : total;
+    const int64_t each = (at1 - at0 + n_warps - 1) / n_warps;
+    u = at0 + warp * each;
+    end = u + each < at1 ? u + each : at1;
+  }
+  // the unit after u where u is past its head's rows
+  __device__ __forceinline__ int64_t skip(int64_t u, int64_t B) const {
+    return b + 1 < B ? (next > u ? next : u + 1) : end;
   }
   __device__ __forceinline__ int64_t head(const int64_t* offsets, int64_t B) const {
     int64_t lo = 0;                                           // largest b whose base is at most u: 32 steps of the
@@ -83,9 +88,9 @@ struct BlockWalk {
       const int lane = threadIdx.x & 31;
       const int64_t step = (n + 31) >> 5, at = lane * step;
       const unsigned below = __ballot_sync(kFullMask, lane == 0 || (at < n && base_of(offsets[lo + at], lo + at) <= u));
-      const int64_t skip = (31 - __clz(below)) * step;
-      lo += skip;
-      n = n - skip < step ? n - skip : step;
+      const int64_t pass = (31 - __clz(below)) * step;
+      lo += pass;
+      n = n - pass < step ? n - pass : step;
     }
     return lo;
   }
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
     fresh = true;
   };
   auto settle = [&]() {                                       // the head's count, once it is there
-    if (fresh && (h.n < 0 || h.n > o1 - h.o || h.n > cap)) {
+    if (fresh && (h.n < 0 || h.o < 0 || h.n > o1 - h.o || h.n > cap)) {
       if (lane == 0) report(status, KVZ_ERR_INVALID_ARG);
       h.n = 0;
     }
@@ -153,8 +158,9 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
   uint8_t* blk = nullptr;
   int rows = 0;                                               // rows of it that count
   int64_t src[2];                                             // element of row r + 8h's first dims here; < 0: zeros
-  auto look_up = [&](int64_t u) {
+  auto look_up = [&]() {
     blk = nullptr;
+    const int64_t u = h.u;
     if (u >= h.end) return;
     while (u >= h.next && h.b + 1 < B) {
       settle();
@@ -166,7 +172,11 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
     const uint32_t q = static_cast<uint32_t>(u - h.base);
     const int32_t id = p0 >= 0 && p0 < cap ? page_id(pg, h.b, q) : -1;
     settle();
-    if (p0 < 0 || p0 >= h.n) return;                          // (below 0: offsets that do not ascend)
+    if (p0 < 0 || p0 >= h.n) {                                // (below 0: offsets that do not ascend)
+      h.u = h.skip(u, B);
+      return;
+    }
+    h.u = u + 1;
     rows = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);
     int32_t from[2];
 #pragma unroll
@@ -181,8 +191,8 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
       else if (c == 0) report(status, KVZ_ERR_INVALID_ARG);   // idx out of [0, n_c): a row of zeros
     }
   };
-  look_up(h.u);
-  for (; h.u < h.end; ++h.u) {
+  look_up();
+  while (blk != nullptr || h.u < h.end) {
     uint8_t* const to = blk;
     const int live = rows;
     uint4 x[2][2][NG][2];                                     // [K, V][row r + 8k][g][half]
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
           x[0][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(K + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
           x[1][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(V + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
         }
-    look_up(h.u + 1);
+    look_up();
     if (to == nullptr) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -284,12 +294,17 @@ __global__ void __launch_bounds__(kC4Threads)
   const uint8_t* blk = nullptr;
   int from = 0, to = 0;                                       // rows of the block that count
   int64_t dst = 0;                                            // output row of the block's row 0
-  auto look_up = [&](int64_t u) {
+  auto look_up = [&]() {
     blk = nullptr;
+    const int64_t u = h.u;
     if (u >= h.end) return;
     while (u >= h.next && h.b + 1 < B) enter(h.b + 1);
     const int64_t q = (h.f >> 4) + u - h.base, p0 = q * kC4Rows;
-    if (q < 0 || p0 >= h.n) return;                           // (below 0: offsets that do not ascend)
+    if (p0 < 0 || p0 >= h.n) {                                // (below 0: offsets that do not ascend)
+      h.u = h.skip(u, B);
+      return;
+    }
+    h.u = u + 1;
     blk = block_at<D>(pg, h.b, static_cast<uint32_t>(q), status);
     from = static_cast<int>(h.f > p0 ? h.f - p0 : 0);
     to = static_cast<int>(h.n - p0 < kC4Rows ? h.n - p0 : kC4Rows);
@@ -307,8 +322,8 @@ __global__ void __launch_bounds__(kC4Threads)
       *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
     }
   };
-  look_up(h.u);
-  for (; h.u < h.end; ++h.u) {
+  look_up();
+  while (blk != nullptr || h.u < h.end) {
     const uint8_t* const p = blk;
     const int lo = from, hi = to;
     const int64_t out = dst;
@@ -326,7 +341,7 @@ __global__ void __launch_bounds__(kC4Threads)
         load_words<2 * NG>(p + L::VS_OFF + (2 * c + 8 * k) * (4 * NG), vs[k]);
       }
     }
-    look_up(h.u + 1);
+    look_up();
     if (p == nullptr) continue;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {

@@ -303,6 +303,22 @@ def test_offsets_that_start_behind_other_rows(counts, page, start, d):
     assert st.item() == 0 and torch.equal(other, cache)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_with_much_room(d):
+    # the last head's room ends at 2^50: what no row fills is passed over, not walked through
+    counts, page = [100, 0, 37, 500], 32
+    cache, pages, n, k, v = filled(counts, d, page, 4)
+    off, st = offsets_of(counts), new_status()
+    off[-1] = 1 << 50
+    got = kvz.kvz_expand_int4(cache, pages, n, off, page, out_rows=sum(counts), status=st)
+    for x, y in zip(got, kvz.kvz_expand_int4(cache, pages, n, offsets_of(counts), page, out_rows=sum(counts))):
+        assert torch.equal(x, y)
+    other = torch.full_like(cache, 255)
+    idx = torch.cat([torch.arange(c, dtype=torch.int32, device="cuda") for c in counts])
+    kvz.kvz_compact_int4(k, v, idx, n, off, other, pages, page, status=st)
+    assert st.item() == 0 and torch.equal(other, cache)
+
+
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
