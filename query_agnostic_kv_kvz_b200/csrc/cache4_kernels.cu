@@ -43,12 +43,12 @@ constexpr int kExpandCtas = 48;                               // several waves (
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
   } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   }
 }
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kC4Threads, 512 / kC4Threads)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const bool on = to != nullptr && r + 8 * k < live && src[k] >= 0;
-          x[0][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(K + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
-          x[1][k][g][j] = on ? __ldg(reinterpret_cast<const uint4*>(V + src[k] + 64 * g + 8 * j)) : make_uint4(0, 0, 0, 0);
+          x[0][k][g][j] = on ? *reinterpret_cast<const uint4*>(K + src[k] + 64 * g + 8 * j) : make_uint4(0, 0, 0, 0);
+          x[1][k][g][j] = on ? *reinterpret_cast<const uint4*>(V + src[k] + 64 * g + 8 * j) : make_uint4(0, 0, 0, 0);
         }
     look_up();
     if (to == nullptr) continue;
@@ -398,8 +398,8 @@ __device__ __forceinline__ void turn_row(uint4& x, int lane, int l, const RotArg
   if (rot.interleaved) {
     if (on && 8 * l < rot.rot) {
       const float* t = rot.table + p * rot.rot + 4 * l;
-      const float4 c = __ldg(reinterpret_cast<const float4*>(t));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(t + rot.rot / 2));
+      const float4 c = *reinterpret_cast<const float4*>(t);
+      const float4 s = *reinterpret_cast<const float4*>(t + rot.rot / 2);
       const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
       turn_neighbours4(x, cc, ss);
     }

@@ -43,7 +43,7 @@ struct C4 {
 // table's width), and the block's address there: null, and a report, for an
 // id outside the pool.
 __device__ __forceinline__ int32_t page_id(const Pages4& pg, int64_t b, uint32_t blk) {
-  return __ldg(pg.pages + b * pg.max_pages + page_of(pg, blk));
+  return pg.pages[b * pg.max_pages + page_of(pg, blk)];
 }
 template <int D>
 __device__ __forceinline__ uint8_t* block_of(const Pages4& pg, int32_t id, uint32_t blk, int32_t* status) {

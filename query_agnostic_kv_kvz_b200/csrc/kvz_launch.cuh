@@ -5,7 +5,10 @@
 // after_prior() before it touches global memory: until then it may only set up
 // shared memory.  after_prior() returns when everything before the launch is
 // complete and visible.  Pointers handed to it come back as new values, so no
-// load through them, read-only or not, can be moved above the wait.
+// load through them can be moved above the wait.  What they point at changes
+// while the kernel is already resident, so it is read by ordinary loads, never
+// by the read-only ones (__ldg, ld.global.nc), which hold for data that stays
+// as it is from the kernel's first instruction to its last.
 #pragma once
 
 #include <cuda_runtime.h>

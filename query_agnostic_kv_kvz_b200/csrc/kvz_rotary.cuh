@@ -14,8 +14,8 @@ __device__ __forceinline__ void load_angles(const float* row, int half, int i0, 
                                             float (&s)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float4 cc = __ldg(reinterpret_cast<const float4*>(row + i0) + h);
-    const float4 ss = __ldg(reinterpret_cast<const float4*>(row + half + i0) + h);
+    const float4 cc = reinterpret_cast<const float4*>(row + i0)[h];
+    const float4 ss = reinterpret_cast<const float4*>(row + half + i0)[h];
     const float sg = inverse ? -1.0f : 1.0f;
     c[4 * h] = cc.x, c[4 * h + 1] = cc.y, c[4 * h + 2] = cc.z, c[4 * h + 3] = cc.w;
     s[4 * h] = sg * ss.x, s[4 * h + 1] = sg * ss.y, s[4 * h + 2] = sg * ss.z, s[4 * h + 3] = sg * ss.w;

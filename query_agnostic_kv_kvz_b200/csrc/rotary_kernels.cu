@@ -29,7 +29,7 @@ constexpr int kRotHeads = 8;                                  // rows a thread w
 // is off by 2^-8 rad), so angle, cosine and sine are float64 and each entry is
 // rounded once.  Run once per model, not on any hot path.
 __global__ void __launch_bounds__(kRotThreads)
-    rotary_table_kernel(const double* __restrict__ freqs, int64_t n, int half, double factor, float* table) {
+    rotary_table_kernel(const double* freqs, int64_t n, int half, double factor, float* table) {
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRotThreads + threadIdx.x; e < n;
        e += static_cast<int64_t>(gridDim.x) * kRotThreads) {
     const int64_t p = e / half;

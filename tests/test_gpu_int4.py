@@ -806,6 +806,46 @@ def test_calls_that_follow_each_other_at_once():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_read_again_after_a_write_between(d):
+    # expand, append, expand, ... with no wait: each reading finds what the writing just before it left, in the same
+    # lines of the same pages; and rows turned in place, compacted, turned on and compacted again
+    page, B, rounds = 16, 40, 12
+    cnt = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cache, pages = pool([16 * 3] * B, d, page, 6)
+    off = offsets_of([1] * B)
+    k = [rand((B, 1, d), 300 + i) for i in range(rounds)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(rounds):                           # the same slot of every head, over and over
+        n, _ = kvz.kvz_append_int4(k[i], k[i], cache, pages, cnt, page)
+        got.append(kvz.kvz_expand_int4(cache, pages, n, off, page, out_rows=B))
+    for i in range(rounds):
+        ref = o4.round_bf16(o4.group_values(*o4.quantize_groups(bits(k[i])[:, 0])))
+        for x in got[i]:
+            np.testing.assert_array_equal(bits(x), ref)
+    t = table(d, 100)
+    n_c = 64
+    pos = torch.full((n_c,), 7, dtype=torch.int32, device="cuda")
+    idx = torch.arange(n_c, dtype=torch.int32, device="cuda").repeat(B)
+    full = torch.full((B,), n_c, dtype=torch.int32, device="cuda")
+    off = offsets_of([n_c] * B)
+    caches = [pool([n_c] * B, d, page, 6) for _ in range(rounds)]
+    x = rand((B, n_c, d), 400)
+    y, want = x.clone(), []
+    for i in range(rounds):
+        y = kvz.kvz_rotary(y, pos, t)
+        torch.cuda.synchronize()
+        want.append(y)
+    for c, p in caches:
+        kvz.kvz_rotary(x, pos, t, out=x)
+        kvz.kvz_compact_int4(x, x, idx, full, off, c, p, page)
+    for (c, p), w in zip(caches, want):
+        other = torch.full_like(c, 255)
+        kvz.kvz_compact_int4(w, w, idx, full, off, other, p, page)
+        assert torch.equal(c, other)
+
+
 def test_two_streams_at_once():
     # the same cache read by two streams, each with its own workspace, and a third call over another cache
     cache, pages, n, _, _ = filled([3000, 12, 9000], 128, 64, 60)

@@ -3,6 +3,9 @@ anything is launched: the Python binding (with a stand-in for the library
 whose compute entry points fail the test), and the C ABI's own checks (the
 real library, which refuses before it touches the GPU).  Runs on the CPU."""
 import ctypes
+import glob
+import os
+import re
 
 import numpy as np
 import pytest
@@ -267,3 +270,14 @@ def test_rotary_freqs():
     r = f4.numpy() / ref
     assert np.allclose(r[turns > 40], 1.0) and np.allclose(r[turns < 0.8], 0.25) and np.all(np.diff(r) <= 1e-12)
     assert np.isclose(a4, 0.1 * np.log(4) + 1)
+
+
+def test_kernels_that_start_early_read_by_ordinary_loads():
+    # they are resident while their inputs are still written, which rules out read-only loads (restrict pointers to
+    # const become such)
+    csrc = os.path.join(os.path.dirname(kvz.__file__), "csrc")
+    text = {p: open(p).read() for p in glob.glob(os.path.join(csrc, "*.cu*"))}
+    early = [p for p, s in text.items() if "after_prior(" in s or p.endswith(("kvz_cache4.cuh", "kvz_rotary.cuh"))]
+    assert len(early) >= 6
+    for p in early:
+        assert not re.search(r"__ldg|\.nc\b|__restrict__", re.sub(r"//[^\n]*", "", text[p])), p
