@@ -19,7 +19,7 @@
 //
 // fp16 operands: q is scaled by a power of two to a largest entry of 2^14
 // (bf16's 8 bits stay exact down to 2^-31 of it); a weight p s, scaled by a
-// power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
+// power of two that follows the largest step (2^-9 at most for p, 2^23 / 2^E
 // for s), is the sum of two fp16 numbers, 22 bits.
 //
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
@@ -68,6 +68,12 @@ constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share i
 constexpr int kD4HeadCost = 40;
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
+// The reference lies 2^16 above the logit that set it, so weights are at most
+// 2^-9 and sums of weighted values leave float32 later than the values' own
+// sum would: V may come as near to its end as quantisation takes it.
+constexpr float kD4Bias = 16.0f;
+// log2 of a softmax denominator: reference M, sum relative to it.
+__device__ __forceinline__ float log2_sum(float M, float sum) { return (M - kD4Bias) + log2f(sum * 0x1p16f); }
 
 template <int D>
 struct D4 {
@@ -389,7 +395,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   float om[NG][2];                                          // sum of p (m + 8 s), the same
 #pragma unroll
   for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
-  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
+  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(23 - E)
 
   bool ok = true;
   for (int i = 0; i < n; ++i) {
@@ -472,7 +478,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
         const float s_new = __uint_as_float(e2 << 23);
         beta = s_top / s_new;                               // 0 the first time
         s_top = s_new;
-        s_mul = __uint_as_float((254u + 7u - e2) << 23);
+        s_mul = __uint_as_float((254u + 23u - e2) << 23);
       }
       float al[2];
 #pragma unroll
@@ -482,9 +488,9 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
         al[e] = 1.0f;
         if (mx > thr[e]) {
-          const float mn = mx * c2[e];
-          al[e] = ex2(-m_neg[e] - mn);                      // 0 the first time
-          m_neg[e] = -mn;
+          const float mn = mx * c2[e], ref = mn + kD4Bias;
+          al[e] = ex2(-m_neg[e] - ref);                     // 0 the first time
+          m_neg[e] = -ref;
           thr[e] = (mn + kD4Slack) / c2[e];
           l_run[e] *= al[e];
 #pragma unroll
@@ -511,7 +517,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
     // ---- out^T += V^T (p s)
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
+      // the weights p s 2^(23 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
       uint32_t hi[2][2], lo[2][2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -561,7 +567,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   if (ok) q.issued -= n;                                      // the rest belongs to the next part
 
   // ---- this head's part is read: the warps' states to shared memory (free again since the CTA's last barrier)
-  const float s_out = s_top * 0x1p2f;                       // 2^E 2^-7 2^9
+  const float s_out = s_top * 0x1p-14f;                     // 2^E 2^-23 2^9
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       if (whole) {
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(part.b) * G * D)[e4] =
             make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[static_cast<int64_t>(part.b) * G + g] = M + log2f(Ls);
+        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[static_cast<int64_t>(part.b) * G + g] = log2_sum(M, Ls);
       } else {
         reinterpret_cast<float4*>(p.part_o + slot * G * D)[e4] = acc;
         if ((4 * e4) % D == 0) p.part_ml[slot * 8 + g] = make_float2(M, Ls);
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   if (e4 < n4 && j == 0) {
     const float inv = 1.0f / Ls;
     reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = M + log2f(Ls);
+    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = log2_sum(M, Ls);
   }
 }
 
@@ -932,7 +938,7 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
     }
     const int64_t at = static_cast<int64_t>(cont.x) * G + g;
     reinterpret_cast<float4*>(p.out + at * D)[tid] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-    if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = M + log2f(Ls);
+    if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = log2_sum(M, Ls);
   }
 }
 

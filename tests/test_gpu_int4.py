@@ -441,6 +441,23 @@ def test_decode_peaked_and_flat(scale):
     check_decode(rand((2, 8, d), 16), cache, pages, n, page, scale)
 
 
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_decode_of_the_largest_values(n):
+    # V near the end of float32: what is finite in the cache and on average stays finite on the way
+    d, page, B = 128, 32, 3
+    k, v = rand((B, n, d), 81), (torch.rand((B, n, d), generator=gen(82), device="cuda") * 2 - 1) * 1.62e38
+    v[..., ::64], v[..., 1::64] = 1.62e38, -1.62e38   # steps of 2^124 and more in every group
+    v[1] = 3.3e38                                     # constant rows: the mean is the largest number there is
+    k[0] = k[0] * torch.linspace(0, 3, n, device="cuda").bfloat16()[:, None]   # logits that climb past the reference
+    cache, pages = pool([n] * B, d, page, 5)
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cnt, _ = kvz.kvz_append_int4(k, v.bfloat16(), cache, pages, zero, page)
+    for p in (pages, wide(pages, page)):
+        for scale in (1e-6, 0.088, 1.0):
+            out, _ = check_decode(rand((B, 4, d), 83), cache, p, cnt, page, scale)
+            assert bool(torch.isfinite(out).all())
+
+
 def test_decode_ignores_rows_past_the_end():
     # NaN scales behind the last row, in its block and on unused pages
     counts, d, page = [1, 18, 47], 128, 16
