@@ -19,7 +19,7 @@
 //
 // fp16 operands: q is scaled by a power of two to a largest entry of 2^14
 // (bf16's 8 bits stay exact down to 2^-31 of it); a weight p s, scaled by a
-// power of two that follows the largest step (2^-9 at most for p, 2^23 / 2^E
+// power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
 // for s), is the sum of two fp16 numbers, 22 bits.
 //
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
@@ -68,12 +68,12 @@ constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share i
 constexpr int kD4HeadCost = 40;
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
-// The reference lies 2^16 above the logit that set it, so weights are at most
-// 2^-9 and sums of weighted values leave float32 later than the values' own
-// sum would: V may come as near to its end as quantisation takes it.
-constexpr float kD4Bias = 16.0f;
-// log2 of a softmax denominator: reference M, sum relative to it.
-__device__ __forceinline__ float log2_sum(float M, float sum) { return (M - kD4Bias) + log2f(sum * 0x1p16f); }
+// Outputs are summed times 2^-16, so they leave float32 later than the values'
+// own sum would, although a weight may be 2^7: V may come as near to float32's
+// end as quantisation takes it.  (As a reference 2^16 higher, which scales the
+// weights themselves, it cost their exponents 4 bits: errors of 4.2e-7 instead
+// of 2.5e-7 of 8 heads of 2,457 rows.)
+constexpr float kD4Out = 0x1p-16f;
 
 template <int D>
 struct D4 {
@@ -139,8 +139,8 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return r;
 }
 // w less the fp16 in the low (high) half of h, exact where h is w rounded; s * f for a
-// bf16 s in the low half of its word and a power of two f; and s * 8 + c.  One mixed
-// instruction each, where widening first would take another.
+// bf16 s in the low half of its word and a power of two f; and (s * 8 + m) kD4Out for
+// the m in its high half.  Mixed instructions, where widening first would take another.
 __device__ __forceinline__ float less_lo(float w, uint32_t h) {
   float d;
   asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, l, m, %2;}" : "=f"(d) : "r"(h), "f"(w));
@@ -157,9 +157,11 @@ __device__ __forceinline__ float step_times(uint32_t s, float f) {
       : "=f"(d) : "r"(s), "r"(__float_as_uint(f)));
   return d;
 }
-__device__ __forceinline__ float step8_plus(uint32_t s, float c) {
+__device__ __forceinline__ float middle(uint32_t w) {
   float d;
-  asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0x4100; fma.rn.f32.bf16 %0, l, m, %2;}" : "=f"(d) : "r"(s), "f"(c));
+  asm("{.reg .b16 l, h, f, f8; .reg .f32 m; mov.b32 {l, h}, %1; mov.b16 f, 0x3780; mov.b16 f8, 0x3900; "
+      "fma.rn.f32.bf16 m, h, f, 0f00000000; fma.rn.f32.bf16 %0, l, f8, m;}"
+      : "=f"(d) : "r"(w));
   return d;
 }
 // 8x8 matrix of 16-bit entries, a row's pair 2c, 2c + 1 in lane (row, c): transposed.
@@ -186,6 +188,12 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
   }
+}
+
+// Summed outputs over their denominator.
+__device__ __forceinline__ float4 quotient(const float4& sum, float Ls) {
+  const float l = Ls * kD4Out;
+  return make_float4(sum.x / l, sum.y / l, sum.z / l, sum.w / l);
 }
 
 // Loads that stay behind the wait for the kernels before this one.
@@ -395,7 +403,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   float om[NG][2];                                          // sum of p (m + 8 s), the same
 #pragma unroll
   for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
-  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(23 - E)
+  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
 
   bool ok = true;
   for (int i = 0; i < n; ++i) {
@@ -478,7 +486,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
         const float s_new = __uint_as_float(e2 << 23);
         beta = s_top / s_new;                               // 0 the first time
         s_top = s_new;
-        s_mul = __uint_as_float((254u + 23u - e2) << 23);
+        s_mul = __uint_as_float((254u + 7u - e2) << 23);
       }
       float al[2];
 #pragma unroll
@@ -488,9 +496,9 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
         al[e] = 1.0f;
         if (mx > thr[e]) {
-          const float mn = mx * c2[e], ref = mn + kD4Bias;
-          al[e] = ex2(-m_neg[e] - ref);                     // 0 the first time
-          m_neg[e] = -ref;
+          const float mn = mx * c2[e];
+          al[e] = ex2(-m_neg[e] - mn);                      // 0 the first time
+          m_neg[e] = -mn;
           thr[e] = (mn + kD4Slack) / c2[e];
           l_run[e] *= al[e];
 #pragma unroll
@@ -517,13 +525,13 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
     // ---- out^T += V^T (p s)
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      // the weights p s 2^(23 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
+      // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
       uint32_t hi[2][2], lo[2][2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float m8 = step8_plus(vp[k][h][g], bf_hi(vp[k][h][g])), sx = step_times(vp[k][h][g], s_mul);
+          const float m8 = middle(vp[k][h][g]), sx = step_times(vp[k][h][g], s_mul);
           const float p0 = x[k][h][0], p1 = x[k][h][1];
           om[g][0] = fmaf(p0, m8, om[g][0]);
           om[g][1] = fmaf(p1, m8, om[g][1]);
@@ -567,7 +575,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   if (ok) q.issued -= n;                                      // the rest belongs to the next part
 
   // ---- this head's part is read: the warps' states to shared memory (free again since the CTA's last barrier)
-  const float s_out = s_top * 0x1p-14f;                     // 2^E 2^-23 2^9
+  const float s_out = s_top * 0x1p-14f;                     // 2^E 2^-7 2^9 kD4Out
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -734,8 +742,8 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
       if (whole) {
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(part.b) * G * D)[e4] =
-            make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[static_cast<int64_t>(part.b) * G + g] = log2_sum(M, Ls);
+            quotient(acc, Ls);
+        if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[static_cast<int64_t>(part.b) * G + g] = M + log2f(Ls);
       } else {
         reinterpret_cast<float4*>(p.part_o + slot * G * D)[e4] = acc;
         if ((4 * e4) % D == 0) p.part_ml[slot * 8 + g] = make_float2(M, Ls);
@@ -856,9 +864,9 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
     acc.z += __shfl_xor_sync(kFullMask, acc.z, o), acc.w += __shfl_xor_sync(kFullMask, acc.w, o);
   }
   if (e4 < n4 && j == 0) {
-    const float inv = 1.0f / Ls;
+    const float inv = 1.0f / (Ls * kD4Out);
     reinterpret_cast<float4*>(p.out + b * G * D)[e4] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = log2_sum(M, Ls);
+    if ((4 * e4) % D == 0 && p.lse2 != nullptr) p.lse2[b * G + 4 * e4 / D] = M + log2f(Ls);
   }
 }
 
@@ -937,8 +945,8 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
       acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
     }
     const int64_t at = static_cast<int64_t>(cont.x) * G + g;
-    reinterpret_cast<float4*>(p.out + at * D)[tid] = make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
-    if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = log2_sum(M, Ls);
+    reinterpret_cast<float4*>(p.out + at * D)[tid] = quotient(acc, Ls);
+    if (tid == 0 && p.lse2 != nullptr) p.lse2[at] = M + log2f(Ls);
   }
 }
 
