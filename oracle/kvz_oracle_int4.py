@@ -13,7 +13,7 @@ import numpy as np
 from oracle.kvz_oracle import bf16_bits_to_f64, decode_attention
 
 __all__ = ["round_bf16", "rotary_table", "rotary", "quantize_groups", "group_values", "block_bytes", "unpack_block",
-           "pack_block", "read_head", "decode_int4", "decode_bound"]
+           "pack_block", "read_head", "decode_int4", "decode_bound", "decode_bound_by_group"]
 
 GROUP = 64
 ROWS = 16
@@ -200,3 +200,41 @@ def decode_bound(q, K, V, scale):
 
     e = (d / 16 + 8) * u * reach(K) * np.abs(q).sum(-1) * scale + 2.0 ** -21
     return 2 * e * np.abs(V).max() + (n / 16 + 32) * u * reach(V), 2 * e / np.log(2.0) + 2.0 ** -20
+
+
+def decode_bound_by_group(q, K, V, scale):
+    """The same per group of 64 dims and weighted by what each row counts for:
+    float64 (out [G, d], bound on |d out| [G, d]) of one head.
+
+    Every float32 step rounds by u = 2^-24 of what it holds, a matrix
+    instruction's sum, which truncates, by 2 u.  With R = range + |min| of a
+    row's group, a logit passes at most d / 16 + 8 such steps over at most
+    sum_groups R sum|q|, a q below 2^-27 of the query's largest entry is held
+    to 2^-35 of it, and the product with the scale and the reference's
+    subtraction add 4 u (max |logit| + 20); exp2 adds 2^-21.  That makes e_j,
+    the relative error of row j's weight.  Weights P_j (1 + e_j), normalised,
+    move the output by at most sum_j P_j e_j (|v_j| + |out|).  A weight times a
+    step is held to u of itself and to 2^-35 of the largest in its group (8
+    codes of it at most are 2^-35 of that row's R), and the sums of what it
+    multiplies round by 2 u of sum_j P_j R_j at most n / 32 + 32 times, the
+    denominator's by as much of the output."""
+    q, K, V = (np.asarray(x, dtype=np.float64) for x in (q, K, V))
+    n, d = K.shape
+    u = 2.0 ** -24
+
+    def reach(x):
+        g = x.reshape(n, -1, GROUP)
+        return (g.max(-1) - g.min(-1)) + np.abs(g.min(-1))                   # [n, NG]
+
+    z = q @ K.T * scale                                                      # [G, n]
+    P = np.exp(z - z.max(-1, keepdims=True))
+    P /= P.sum(-1, keepdims=True)
+    out = P @ V
+    qa = np.abs(q).reshape(q.shape[0], -1, GROUP).sum(-1)                    # [G, NG]
+    e = (d / 16 + 8) * 2 * u * (qa @ reach(K).T) * scale
+    e += 2.0 ** -35 * np.abs(q).max(-1, keepdims=True) * GROUP * reach(K).sum(-1)[None] * scale
+    e += 4 * u * (np.abs(z).max(-1, keepdims=True) + 20) + 2.0 ** -21
+    steps = (n / 32 + 32) * 2 * u
+    sums = np.repeat(P @ reach(V), GROUP, axis=-1)
+    rest = np.repeat((P[..., None] * reach(V)[None]).max(1), GROUP, axis=-1) * n * 2.0 ** -35
+    return out, rest + (P * e) @ np.abs(V) + (P * e).sum(-1, keepdims=True) * np.abs(out) + steps * (sums + np.abs(out))

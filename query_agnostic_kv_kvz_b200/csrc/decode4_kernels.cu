@@ -17,10 +17,16 @@
 // adds to, so it sums 32 rows at a time and the running output adds those in
 // float32.
 //
-// fp16 operands: q is scaled by a power of two to a largest entry of 2^14
-// (bf16's 8 bits stay exact down to 2^-31 of it); a weight p s, scaled by a
-// power of two that follows the largest step (2^7 at most for p, 2^7 / 2^E
-// for s), is the sum of two fp16 numbers, 22 bits.
+// fp16 operands.  q is scaled by a power of two to a largest entry of 2^14
+// (and half of the dims by 1/16 more): its 8 bits stay exact down to 2^-27 of
+// the largest entry, and what is smaller is held to 2^-35 of it.  A weight p s
+// is the sum of two fp16 numbers, hi + lo, after a power of two of its own
+// query and group of 64 dims, which follows the largest weight so far: it is
+// held to 2^-24 of itself, as float32 holds it, and to 2^-35 of that largest.
+// So neither the other group's steps nor a row of large values that hardly
+// counts costs a group its bits.  (Three bf16 numbers, which need no power of
+// two: 87.4 us against 77.9 for the heads below; one power for all that a warp
+// reads, which loses the smaller group's bits: 76.4.)
 //
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
 // rate an SM would have to widen and multiply a row (both of K and V, all
@@ -75,6 +81,15 @@ constexpr float kD4Slack = 7.0f;                              // log2 by which a
 // of 2.5e-7 of 8 heads of 2,457 rows.)
 constexpr float kD4Out = 0x1p-16f;
 
+// Weights p s go to fp16 times a power of two per query and group that follows
+// the largest of them: one past kD4WeightTop brings it down so that the stage's
+// largest is between 2^10 and 2^11, and it grows again as weights shrink under
+// a reference that moves.
+constexpr float kD4WeightTop = 32768.0f;
+constexpr float kD4MulTop = 0x1p110f;                         // where the power begins
+__device__ __forceinline__ uint32_t field(float x) { return __float_as_uint(x) >> 23; }
+__device__ __forceinline__ float power(uint32_t field) { return __uint_as_float(field << 23); }
+
 template <int D>
 struct D4 {
   static constexpr int KS = D / 16;                           // k-steps of Q K^T
@@ -105,6 +120,11 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, f
       "mov.b64 {%0, %1}, x;}"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -170,12 +190,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 template <int N>
 __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "");
@@ -395,7 +409,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
     }
   }
 
-  float o[S::MT][4];                                        // out^T tiles / 2^E: dims x queries 2c, 2c + 1
+  float o[S::MT][4];                                        // out^T tiles (dims x queries 2c, 2c + 1) times mul
 #pragma unroll
   for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
   float m_neg[2] = {INFINITY, INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // -reference of queries 2c, 2c + 1
@@ -403,7 +417,9 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   float om[NG][2];                                          // sum of p (m + 8 s), the same
 #pragma unroll
   for (int g = 0; g < NG; ++g) om[g][0] = om[g][1] = 0.0f;
-  float s_top = 0.0f, s_mul = 0.0f;                         // 2^E, above every step so far, and 2^(7 - E)
+  float mul[NG][2];                                         // the weights' power of two, the same
+#pragma unroll
+  for (int g = 0; g < NG; ++g) mul[g][0] = mul[g][1] = kD4MulTop;
 
   bool ok = true;
   for (int i = 0; i < n; ++i) {
@@ -466,50 +482,33 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
             for (int g = 0; g < NG; ++g) vp[k][h][g] = 0u;
           }
     }
-    // ---- softmax against references that move only when a logit passes them by 2^7; the steps' scale likewise
+    // ---- softmax against references that move only when a logit passes them by 2^7
     float xm[2];
-    uint32_t vmax = 0u;
 #pragma unroll
     for (int e = 0; e < 2; ++e) xm[e] = fmaxf(max3(x[0][0][e], x[0][1][e], x[1][0][e]), x[1][1][e]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) vmax = max_bf2(vmax, vp[k][h][g]);
-    if (__any_sync(kFullMask, xm[0] > thr[0] || xm[1] > thr[1] || bf_lo(vmax) > s_top)) {
-      // the power of two past the largest step (at least 2^-100, at most 2^126), twice that for room
-      const uint32_t top = __reduce_max_sync(kFullMask, __float_as_uint(bf_lo(vmax)));
-      float beta = 1.0f;
-      if (__uint_as_float(top) > s_top) {
-        const uint32_t e2 = min(max((top >> 23) + 2u, 27u), 253u);
-        const float s_new = __uint_as_float(e2 << 23);
-        beta = s_top / s_new;                               // 0 the first time
-        s_top = s_new;
-        s_mul = __uint_as_float((254u + 7u - e2) << 23);
-      }
-      float al[2];
+    if (__any_sync(kFullMask, xm[0] > thr[0] || xm[1] > thr[1])) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx = xm[e];
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, sh));
-        al[e] = 1.0f;
         if (mx > thr[e]) {
           const float mn = mx * c2[e];
-          al[e] = ex2(-m_neg[e] - mn);                      // 0 the first time
+          const float al = ex2(-m_neg[e] - mn);             // 0 the first time
           m_neg[e] = -mn;
           thr[e] = (mn + kD4Slack) / c2[e];
-          l_run[e] *= al[e];
+          l_run[e] *= al;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) om[g][e] *= al[e];
+          for (int g = 0; g < NG; ++g) {
+            om[g][e] *= al;
+            // weights shrink by al, so their power of two grows by as many bits
+            const uint32_t now = field(mul[g][e]), to = min(now + 127u - field(al), field(kD4MulTop));
+            const float f = al * power(127u + min(to - now, 127u));
+            mul[g][e] = power(to);
+#pragma unroll
+            for (int t = 4 * g; t < 4 * g + 4; ++t) o[t][e] *= f, o[t][2 + e] *= f;
+          }
         }
-        al[e] *= beta;
-      }
-#pragma unroll
-      for (int t = 0; t < S::MT; ++t) {
-        o[t][0] *= al[0], o[t][1] *= al[1];
-        o[t][2] *= al[0], o[t][3] *= al[1];
       }
     }
 #pragma unroll
@@ -522,23 +521,60 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
         add2(l_run[0], l_run[1], x[k][h][0], x[k][h][1]);
       }
 
+    // ---- the weights p s times their power of two
+    float w[NG][2][2][2], wm = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float m8 = middle(vp[k][h][g]);
+          float y0 = x[k][h][0], y1 = x[k][h][1];
+          fma2(y0, y1, m8, m8, om[g][0], om[g][1]);
+          om[g][0] = y0, om[g][1] = y1;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[g][k][h][e] = step_times(vp[k][h][g], mul[g][e]);
+          mul2(w[g][k][h][0], w[g][k][h][1], x[k][h][0], x[k][h][1]);
+          wm = max3(wm, w[g][k][h][0], w[g][k][h][1]);
+        }
+    if (__any_sync(kFullMask, wm > kD4WeightTop)) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = 0.0f;                                   // the stage's largest weight
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) top = fmaxf(top, x[k][h][e] * bf_lo(vp[k][h][g]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, sh));
+          const uint32_t now = field(mul[g][e]), to = min(now, 264u - field(top));
+          const float f = power(127u - min(now - to, 127u));  // (past 2^-126: 0)
+          mul[g][e] = power(to);
+#pragma unroll
+          for (int t = 4 * g; t < 4 * g + 4; ++t) o[t][e] *= f, o[t][2 + e] *= f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[g][k][h][e] = x[k][h][e] * step_times(vp[k][h][g], mul[g][e]);
+        }
+    }
+
     // ---- out^T += V^T (p s)
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      // the weights p s 2^(7 - E) = hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
+      // the weights as hi + lo in fp16, transposed from (key r; queries) to (query r; keys 2c, 2c + 1)
       uint32_t hi[2][2], lo[2][2];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float m8 = middle(vp[k][h][g]), sx = step_times(vp[k][h][g], s_mul);
-          const float p0 = x[k][h][0], p1 = x[k][h][1];
-          om[g][0] = fmaf(p0, m8, om[g][0]);
-          om[g][1] = fmaf(p1, m8, om[g][1]);
-          const float w0 = p0 * sx, w1 = p1 * sx;
-          const uint32_t w = pack_h2(w0, w1);
-          hi[k][h] = transpose8(w);
-          lo[k][h] = transpose8(pack_h2(less_lo(w0, w), less_hi(w1, w)));
+          const uint32_t part = pack_h2(w[g][k][h][0], w[g][k][h][1]);
+          hi[k][h] = transpose8(part);
+          lo[k][h] = transpose8(pack_h2(less_lo(w[g][k][h][0], part), less_hi(w[g][k][h][1], part)));
         }
       __syncwarp();
       uint32_t vw[2][2][2];
@@ -575,7 +611,6 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   if (ok) q.issued -= n;                                      // the rest belongs to the next part
 
   // ---- this head's part is read: the warps' states to shared memory (free again since the CTA's last barrier)
-  const float s_out = s_top * 0x1p-14f;                     // 2^E 2^-7 2^9 kD4Out
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -591,6 +626,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float* d0 = s_o + (warp * 8 + 2 * c + e) * D + 64 * g + 8 * r;
+      const float s_out = kD4Out * 0x1p9f * power(254u - field(mul[g][e]));
 #pragma unroll
       for (int wl = 0; wl < 2; ++wl) {
         const float(&x0)[4] = o[4 * g + 2 * wl], (&x1)[4] = o[4 * g + 2 * wl + 1];

@@ -458,6 +458,44 @@ def test_decode_of_the_largest_values(n):
             assert bool(torch.isfinite(out).all())
 
 
+SPREADS = {
+    # what row j and group g of V are multiplied by
+    "second group 2^-10": lambda n, NG: torch.tensor([1.0, 2.0 ** -10])[:NG].expand(n, NG),
+    "second group 2^-14": lambda n, NG: torch.tensor([1.0, 2.0 ** -14])[:NG].expand(n, NG),
+    "second group 2^-40": lambda n, NG: torch.tensor([2.0 ** 20, 2.0 ** -20])[:NG].expand(n, NG),
+    "last rows 2^-12": lambda n, NG: torch.where(torch.arange(n)[:, None] < n // 4, 1.0, 2.0 ** -12).expand(n, NG),
+    "one row 2^20": lambda n, NG: torch.where(torch.arange(n)[:, None] == 5 % n, 2.0 ** 20, 1.0).expand(n, NG),
+    "one row 2^30": lambda n, NG: torch.where(torch.arange(n)[:, None] == 5 % n, 2.0 ** 30, 1.0).expand(n, NG),
+    "one row 2^90": lambda n, NG: torch.where(torch.arange(n)[:, None] == 5 % n, 2.0 ** 90, 1.0).expand(n, NG),
+    "rows and groups 2^-60 to 2^60": lambda n, NG: 2.0 ** torch.randint(
+        -60, 61, (n, NG), generator=torch.Generator().manual_seed(n)).double(),
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("name", SPREADS)
+@pytest.mark.parametrize("n", [40, 2500])
+def test_decode_of_values_of_very_different_size(n, name, d):
+    # every group's output is held to its own size, whatever the other group's steps and those of rows that hardly
+    # count: with "one row", that row's logit is far below the others'
+    page, G = 32, 4
+    mul = SPREADS[name](n, d // 64).double().repeat_interleave(64, 1).cuda()
+    v = (torch.randn((1, n, d), generator=gen(84), device="cuda").double() * mul).bfloat16()
+    base = rand((1, 1, d), 85)
+    q = (base + 0.1 * rand((1, G, d), 86)).bfloat16()
+    k = rand((1, n, d), 87)
+    if name.startswith("one row"):
+        k[:, 5 % n] = -8.0 * base[:, 0]               # at d = 64 a logit of about -60 against +-8
+    cache, pages = pool([n], d, page, 5)
+    cnt, _ = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros(1, dtype=torch.int32, device="cuda"), page)
+    K, V = o4.read_head(cache.cpu().numpy(), pages[0].cpu().numpy(), page, d, n)
+    want, tol = o4.decode_bound_by_group(f64(q)[0], K, V, d ** -0.5)
+    for p in (pages, wide(pages, page)):
+        got = kvz.kvz_decode_int4(q, cache, p, cnt, page)[0][0].cpu().double().numpy()
+        off = np.abs(got - want) / tol
+        assert np.all(off <= 1), (off.max(), np.abs(got - want).max())
+
+
 def test_decode_ignores_rows_past_the_end():
     # NaN scales behind the last row, in its block and on unused pages
     counts, d, page = [1, 18, 47], 128, 16
