@@ -481,7 +481,8 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /* of that head means nothing), an idx outside [0, n_c) (a row of zeros), a  */
 /* position outside the table or n_new outside [0, T] or past the table's    */
 /* last page (not appended; counts_out[b] = counts[b]), an output row past   */
-/* n_rows (the head is left out).                                            */
+/* n_rows (the head is left out).  If attention's wait for rows expires      */
+/* (KVZ_ERR_TIMEOUT), the heads that were still to be read are NaN.          */
 /* ------------------------------------------------------------------------ */
 size_t kvz_cache4_page_bytes(int page_size, int d);
 

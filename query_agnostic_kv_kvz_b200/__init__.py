@@ -26,6 +26,7 @@ __all__ = [
     "kvz_select_protected", "kvz_compact_int8", "kvz_rotary_freqs", "kvz_rotary_table", "kvz_rotary",
     "kvz_cache4_page_bytes", "kvz_compact_int4", "kvz_append_int4", "kvz_expand_int4",
     "kvz_decode_int4_workspace_size", "kvz_decode_int4", "kvz_testing_compact_in_place_withhold",
+    "kvz_testing_decode_int4_withhold",
 ]
 
 PER_HEAD = 0
@@ -101,6 +102,8 @@ _SIGS = {
     "kvz_decode_int4_workspace_size": (_sz, [_i64, _i32, _i64, _i32]),
     "kvz_decode_int4": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp,
                                _vp]),
+    "kvz_testing_decode_int4_withhold": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp,
+                                                _vp, _sz, _i64, _i64, _i64, _vp, _vp]),
     "kvz_testing_compact_in_place_withhold": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _i64, _i64,
                                                      _i64, _vp, _vp]),
 }
@@ -1266,3 +1269,35 @@ def kvz_testing_compact_in_place_withhold(K, V, idx, counts, offsets, wait_ns: i
             _ptr(K), _ptr(V), B, n_c, d, _ptr(idx), _ptr(counts), _ptr(offsets), _ptr(workspace), _bytes(workspace),
             int(wait_ns), int(hold_head), int(hold_chunk), _ptr(status), _stream(stream)))
     return K, V
+
+
+def kvz_testing_decode_int4_withhold(q, cache, pages, counts, page_size: int, wait_ns: int, hold_head: int,
+                                     hold_cta: int = -1, out=None, lse2=None, workspace=None, status=None):
+    """Test-only (include/kvz_testing.h): kvz_decode_int4 whose waits give up
+    after ``wait_ns`` and in which the first rows of head ``hold_head`` never
+    arrive at warp 0 of CTA ``hold_cta`` (-1: of every CTA that reads it).
+    Returns (out, lse2); the heads such a CTA still had to read are NaN."""
+    fn = "kvz_testing_decode_int4_withhold"
+    _vec(fn, "q", q, _bf16, 0, required=True)
+    B, G, d = q.shape
+    _table_rows(fn, _cache4(fn, cache, pages, page_size, d)[1], B)
+    _vec(fn, "counts", counts, _i32t, B, required=True)
+    _dense(fn, "out", out, _f32, q.shape)
+    _dense(fn, "lse2", lse2, _f32, q.shape[:2])
+    _vec(fn, "workspace", workspace, _u8, 0)
+    _vec(fn, "status", status, _i32t, 1)
+    dev = _one_device(fn, q, cache, pages, counts, out, lse2, workspace, status)
+    with _on(fn, dev, None):
+        if out is None:
+            out = torch.empty(q.shape, dtype=_f32, device=dev)
+        if lse2 is None:
+            lse2 = torch.empty((B, G), dtype=_f32, device=dev)
+        if workspace is None:
+            workspace = torch.empty((lib().kvz_decode_int4_workspace_size(B, G, pages.shape[1] * page_size, d),),
+                                    dtype=_u8, device=dev)
+        _check(fn, lib().kvz_testing_decode_int4_withhold(
+            q.data_ptr(), cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(), pages.shape[1],
+            counts.data_ptr(), B, G, d, d ** -0.5, out.data_ptr(), lse2.data_ptr(),
+            workspace.data_ptr() if workspace.numel() else None, workspace.numel(), int(wait_ns), int(hold_head),
+            int(hold_cta), _addr(status), _raw(dev)))
+    return out, lse2

@@ -43,7 +43,8 @@
 // output) per query; the warps merge in shared memory at the end of each
 // head's part.  A head that several CTAs read leaves one partial per CTA,
 // which a second launch joins in order: no atomics, and identical inputs give
-// identical results.  (One CTA of 16 warps per SM: 82.3 against 81 us, and
+// identical results.  A wait that expires makes NaN of the heads that its CTA
+// still had to read.  (One CTA of 16 warps per SM: 82.3 against 81 us, and
 // 31.9 against 24.3 at 96 uneven heads; 12 warps of 168 registers: 88.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -268,7 +269,7 @@ struct Part4 {
 // A warp's ring of stages, kept full across the parts that its CTA reads one
 // after another.  Where stages lie in the pool is looked up 32 at a time, a
 // lane each.
-template <int D>
+template <int D, bool TEST>
 struct Ring4 {
   uint8_t* ring;
   uint64_t* bar;
@@ -305,6 +306,7 @@ struct Ring4 {
     using L = C4<D>;
     if ((i & 31) == 0 && !(placed && i == 0)) look_up(p, t, warp, i + lane, spread);
     const int from0 = __shfl_sync(kFullMask, at0, i & 31), from1 = __shfl_sync(kFullMask, at1, i & 31);
+    if (TEST && i == 0 && warp == 0 && t.b == p.hold_head && (p.hold_cta < 0 || blockIdx.x == p.hold_cta)) return;
     if (lane == 0) {
       const uint32_t st = (used + static_cast<uint32_t>(ahead)) % kD4Stages;
       uint8_t* const dst = ring + st * D4<D>::STAGE;
@@ -351,9 +353,9 @@ struct Query4 {
 // reference, sum and output per query in shared memory.  `then` (in shared
 // memory) is the part that the CTA reads next.  False in a warp whose wait
 // expired.
-template <int D>
+template <int D, bool TEST>
 __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& query, const Part4& part,
-                                          const Part4* then, Ring4<D>& q,
+                                          const Part4* then, Ring4<D, TEST>& q,
                                           volatile int* abort_flag, float* s_o, float (*s_m)[8], float (*s_l)[8],
                                           int spread) {
   using L = C4<D>;
@@ -424,7 +426,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
   bool ok = true;
   for (int i = 0; i < n; ++i) {
     const uint32_t st = q.used % kD4Stages;
-    ok = mbar_wait_warp(&q.bar[st], (q.used / kD4Stages) & 1u, abort_flag, p.status);
+    ok = mbar_wait_warp(&q.bar[st], (q.used / kD4Stages) & 1u, abort_flag, p.status, TEST ? p.wait_ns : kWaitLimitNs);
     if (!ok) {                                                // warp-uniform
       q.drain(lane, i);
       break;
@@ -663,7 +665,7 @@ __device__ __forceinline__ float4 join_warps(int e4, const float* s_o, const flo
   return acc;
 }
 
-template <int D>
+template <int D, bool TEST>
 __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) {
   using S = D4<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -746,10 +748,11 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
     return;
   }
 
-  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, false};
+  Ring4<D, TEST> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, false};
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
   int4 cont = make_int4(-1, 0, 0, 0);
 
+  bool failed = false;
   for (;;) {
     Query4<D> query;                                          // on its way before the first stages are issued
     query.load(p, part.b);
@@ -764,11 +767,10 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       }
     }
     __syncthreads();                                          // also: the warps' states of the last part are read
-    const bool ok = read_part<D>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, 0);
-    if (__syncthreads_or(!ok)) {                              // uniform: the output of this share is not written
-      if (ok) ring.drain(lane, 0);
-      if (tid == 0) p.cont[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      return;
+    if (!failed) {
+      const bool ok = read_part<D, TEST>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, 0);
+      failed = __syncthreads_or(!ok);                         // uniform: the share's heads from this one on come out as
+      if (failed && ok) ring.drain(lane, 0);                  // NaN, also those that other CTAs read a part of
     }
     const bool whole = part.a0 == 0 && part.a1 == n_blk, past = part.a1 < n_blk;
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (past ? 1 : 0);
@@ -776,6 +778,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_kernel(Dec4Args p) 
       const int g = 4 * e4 / D;
       float M, Ls;
       const float4 acc = join_warps<D>(e4, s_o, s_m, s_l, M, Ls);
+      if (failed) Ls = NAN;
       if (whole) {
         reinterpret_cast<float4*>(p.out + static_cast<int64_t>(part.b) * G * D)[e4] =
             quotient(acc, Ls);
@@ -822,7 +825,7 @@ __device__ __forceinline__ void send(uint32_t at, const float2& v, uint32_t bar)
 // chain of calls, of which the first 1.6 pass before the first rows are there
 // (count and page, then rows) and 1.2 in the join; a microsecond more when
 // every CTA fetched the others' states, two round trips and a barrier more.
-template <int D>
+template <int D, bool TEST>
 __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4Args p) {
   using S = D4<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -851,7 +854,7 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   // stages in turn over the cluster's CTAs and their warps, so that where a warp's stages are does not depend on the
   // head's rows: their pages are looked up beside the count
   const int lane = tid & 31, blk = 2 * (rank + C * (warp + kD4Warps * lane)), tab = static_cast<int>(p.cap / kC4Rows);
-  const int2 early = blk < tab ? Ring4<D>::ids(p, static_cast<int>(b), blk, tab) : make_int2(0, 0);
+  const int2 early = blk < tab ? Ring4<D, TEST>::ids(p, static_cast<int>(b), blk, tab) : make_int2(0, 0);
   const int count = load_int(p.counts + b);                   // the same in all CTAs of the cluster
   Query4<D> query;
   query.load(p, b);
@@ -868,11 +871,11 @@ __global__ void __launch_bounds__(kD4Threads, 2) decode_int4_cluster_kernel(Dec4
   const Part4 part{static_cast<int>(b), count, 2 * rank, (count + kC4Rows - 1) / kC4Rows};
   const int spread = 31 - __clz(C);                           // (C is a power of two)
   float* s_o = reinterpret_cast<float*>(smem + S::O_OFF);
-  Ring4<D> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, true};
+  Ring4<D, TEST> ring{smem + warp * (kD4Stages * S::STAGE), full + warp * kD4Stages, 0u, 0, 0, 0, true};
   if (blk < part.a1) ring.place(p, make_int2(early.x, blk + 1 < part.a1 ? early.y : early.x), blk);
   if (tid == 0) s_then.b = -1;
   __syncthreads();                                            // the barriers are initialised
-  const bool ok = read_part<D>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, spread);
+  const bool ok = read_part<D, TEST>(p, query, part, &s_then, ring, &s_abort, s_o, s_m, s_l, spread);
   const bool failed = __syncthreads_or(!ok);
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < n4) {                                             // n4 <= 2 D <= kD4Threads
@@ -986,21 +989,21 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
   }
 }
 
-template <int D>
+template <int D, bool TEST>
 cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
   const Decode4Form form = decode4_form(a.B, a.cap);
   if (form.cluster > 0) {
     constexpr int kAlone = 115 * 1024;                        // of an SM's 228 KB: one CTA
     static_assert(D4<D>::SMEM <= kAlone, "");
-    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D>>(kAlone);
-    if (e == cudaSuccess && form.cluster > 8) e = wide_clusters_once<decode_int4_cluster_kernel<D>>();
+    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D, TEST>>(kAlone);
+    if (e == cudaSuccess && form.cluster > 8) e = wide_clusters_once<decode_int4_cluster_kernel<D, TEST>>();
     if (e != cudaSuccess) return e;
-    return launch_after(decode_int4_cluster_kernel<D>, dim3(static_cast<unsigned>(a.B * form.cluster)), dim3(kD4Threads),
+    return launch_after(decode_int4_cluster_kernel<D, TEST>, dim3(static_cast<unsigned>(a.B * form.cluster)), dim3(kD4Threads),
                         form.alone ? kAlone : D4<D>::SMEM, stream, form.cluster, a);
   }
-  cudaError_t e = smem_limit_once<decode_int4_kernel<D>>(D4<D>::SMEM);
+  cudaError_t e = smem_limit_once<decode_int4_kernel<D, TEST>>(D4<D>::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_after(decode_int4_kernel<D>, dim3(kD4Workers), dim3(kD4Threads), D4<D>::SMEM, stream, 0, a);
+  e = launch_after(decode_int4_kernel<D, TEST>, dim3(kD4Workers), dim3(kD4Threads), D4<D>::SMEM, stream, 0, a);
   if (e != cudaSuccess) return e;
   return launch_after(merge_int4_kernel<D>, dim3(kD4Workers, static_cast<unsigned>(a.G)), dim3(kD4Threads), 0, stream, 0,
                       a);
@@ -1009,7 +1012,8 @@ cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_decode_int4(int d, const Dec4Args& a, cudaStream_t stream) {
-  return d == 128 ? launch_decode4<128>(a, stream) : launch_decode4<64>(a, stream);
+  if (a.wait_ns > 0) return d == 128 ? launch_decode4<128, true>(a, stream) : launch_decode4<64, true>(a, stream);
+  return d == 128 ? launch_decode4<128, false>(a, stream) : launch_decode4<64, false>(a, stream);
 }
 
 }  // namespace kvz

@@ -7,6 +7,7 @@
 
 #include "kvz.h"
 #include "kvz_internal.h"
+#include "kvz_testing.h"
 
 namespace {
 
@@ -46,6 +47,37 @@ kvz_status check_rotation(const int32_t* positions, int64_t pos_sb, const float*
   if (!aligned(positions, 4) || !aligned(table, 16)) return KVZ_ERR_ALIGNMENT;
   *r = kvz::RotArgs{positions, pos_sb, table, n_pos, rot, interleaved, inverse};
   return KVZ_OK;
+}
+
+kvz_status decode_int4(const void* q, const void* cache, int64_t n_pages, int page_size, const int32_t* pages,
+                       int64_t max_pages, const int32_t* counts, int64_t B, int G, int d, float scale, float* out,
+                       float* lse2, void* workspace, size_t workspace_bytes, uint64_t wait_ns, int64_t hold_head,
+                       int64_t hold_cta, int32_t* d_status, cudaStream_t stream) {
+  if (q == nullptr || counts == nullptr || out == nullptr) return KVZ_ERR_INVALID_ARG;
+  kvz::Dec4Args a{};
+  const kvz_status st = check_pages(cache, n_pages, page_size, pages, max_pages, B, d, &a.pg);
+  if (st != KVZ_OK) return st;
+  if (G < 1 || G > kvz::kDecGMax) return KVZ_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return KVZ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4) || !aligned(lse2, 4)) return KVZ_ERR_ALIGNMENT;
+  const size_t need = kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KVZ_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KVZ_ERR_ALIGNMENT;
+  a.B = B, a.G = G;
+  a.cap = max_pages * page_size;
+  a.c2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.q = static_cast<const uint16_t*>(q);
+  a.counts = counts;
+  a.out = out, a.lse2 = lse2;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.cont = reinterpret_cast<int4*>(w);
+  w += up256(kvz::kD4Workers * sizeof(int4));
+  a.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(2 * kvz::kD4Workers * 8 * sizeof(float2));
+  a.part_o = reinterpret_cast<float*>(w);
+  a.status = d_status;
+  a.wait_ns = wait_ns, a.hold_head = hold_head, a.hold_cta = hold_cta;
+  return kvz::launch_decode_int4(d, a, stream) == cudaSuccess ? KVZ_OK : KVZ_ERR_CUDA;
 }
 
 }  // namespace
@@ -173,30 +205,19 @@ kvz_status kvz_decode_int4(const void* q, const void* cache, int64_t n_pages, in
                            int64_t max_pages, const int32_t* counts, int64_t B, int G, int d, float scale, float* out,
                            float* lse2, void* workspace, size_t workspace_bytes, int32_t* d_status,
                            cudaStream_t stream) {
-  if (q == nullptr || counts == nullptr || out == nullptr) return KVZ_ERR_INVALID_ARG;
-  kvz::Dec4Args a{};
-  const kvz_status st = check_pages(cache, n_pages, page_size, pages, max_pages, B, d, &a.pg);
-  if (st != KVZ_OK) return st;
-  if (G < 1 || G > kvz::kDecGMax) return KVZ_ERR_UNSUPPORTED;
-  if (!std::isfinite(scale) || !(scale > 0.0f)) return KVZ_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(counts, 4) || !aligned(lse2, 4)) return KVZ_ERR_ALIGNMENT;
-  const size_t need = kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KVZ_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return KVZ_ERR_ALIGNMENT;
-  a.B = B, a.G = G;
-  a.cap = max_pages * page_size;
-  a.c2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  a.q = static_cast<const uint16_t*>(q);
-  a.counts = counts;
-  a.out = out, a.lse2 = lse2;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  a.cont = reinterpret_cast<int4*>(w);
-  w += up256(kvz::kD4Workers * sizeof(int4));
-  a.part_ml = reinterpret_cast<float2*>(w);
-  w += up256(2 * kvz::kD4Workers * 8 * sizeof(float2));
-  a.part_o = reinterpret_cast<float*>(w);
-  a.status = d_status;
-  return kvz::launch_decode_int4(d, a, stream) == cudaSuccess ? KVZ_OK : KVZ_ERR_CUDA;
+  return decode_int4(q, cache, n_pages, page_size, pages, max_pages, counts, B, G, d, scale, out, lse2, workspace,
+                     workspace_bytes, 0, -1, -1, d_status, stream);
+}
+
+kvz_status kvz_testing_decode_int4_withhold(const void* q, const void* cache, int64_t n_pages, int page_size,
+                                            const int32_t* pages, int64_t max_pages, const int32_t* counts, int64_t B,
+                                            int G, int d, float scale, float* out, float* lse2, void* workspace,
+                                            size_t workspace_bytes, int64_t wait_ns, int64_t hold_head,
+                                            int64_t hold_cta, int32_t* d_status, cudaStream_t stream) {
+  if (wait_ns < 1000 || wait_ns > 1000000000 || hold_head < 0 || hold_head >= B || hold_cta < -1)
+    return KVZ_ERR_INVALID_ARG;
+  return decode_int4(q, cache, n_pages, page_size, pages, max_pages, counts, B, G, d, scale, out, lse2, workspace,
+                     workspace_bytes, static_cast<uint64_t>(wait_ns), hold_head, hold_cta, d_status, stream);
 }
 
 }  // extern "C"

@@ -246,6 +246,9 @@ struct Dec4Args {
   float2* part_ml;                          // [2 * kD4Workers][8] partial (reference, sum)
   float* part_o;                            // [2 * kD4Workers][G][d]
   int32_t* status;
+  // the test entry point's only: its waits' limit, and the head and CTA (-1: any) whose first stage stays away
+  uint64_t wait_ns = 0;
+  int64_t hold_head = -1, hold_cta = -1;
 };
 // The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
 // table holds `cap` rows, or 0 for shares of equal work; `alone`: each on an SM

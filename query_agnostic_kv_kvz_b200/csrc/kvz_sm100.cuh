@@ -81,9 +81,9 @@ __device__ __forceinline__ uint32_t mbar_try_wait_hint(uint64_t* bar, uint32_t p
 
 // Bounded wait for the phase of `bar` with the given parity to complete.
 // Returns false if the CTA-wide abort flag is raised or the wait exceeds
-// kWaitLimitNs (then it raises the flag and records KVZ_ERR_TIMEOUT).
+// limit_ns (then it raises the flag and records KVZ_ERR_TIMEOUT).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int32_t* status) {
+                                          int32_t* status, uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   uint32_t it = 0;
@@ -92,7 +92,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       return true;
     if ((++it & 15u) == 0u) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (globaltimer_ns() - t0 > limit_ns) {
         *abort_flag = 1;
         report(status, KVZ_ERR_TIMEOUT);
         return false;
@@ -104,8 +104,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // Warp-uniform form of mbar_wait for warps that go on to run .sync.aligned
 // instructions (tcgen05.ld): every lane gets the same answer.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                               int32_t* status) {
-  const bool ok = mbar_wait(bar, parity, abort_flag, status);
+                                               int32_t* status, uint64_t limit_ns = kWaitLimitNs) {
+  const bool ok = mbar_wait(bar, parity, abort_flag, status, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 
