@@ -130,7 +130,7 @@ def lib():
 
 
 # The short way into the decoding calls (csrc/fast_calls.cpp), once the library
-# is loaded and if the module was built for this torch: same checks, same C
+# is loaded and if the module was built for this torch and this C ABI: same checks, same C
 # calls, same results, less host time.  It answers None for anything unusual,
 # which then goes through the checks below.
 _fast = None
@@ -140,9 +140,10 @@ def _load_fast():
     global _fast
     try:
         from . import _kvz_fast as m
-    except ImportError:
-        return
-    if m.torch_version != torch.__version__:
+        from .build import header_id
+        if m.torch_version != torch.__version__ or getattr(m, "header_id", None) != header_id():
+            return
+    except (ImportError, OSError):                    # not built, or no header to compare with
         return
     m.bind(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in
              ("kvz_rotary", "kvz_compact_int4", "kvz_append_int4", "kvz_expand_int4", "kvz_decode_int4",

@@ -379,7 +379,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvz_fast", nullptr, -1, methods, 
 
 PyMODINIT_FUNC PyInit__kvz_fast(void) {
   PyObject* const m = PyModule_Create(&module);
-  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", KVZ_TORCH_VERSION) != 0) {
+  if (m != nullptr && (PyModule_AddStringConstant(m, "torch_version", KVZ_TORCH_VERSION) != 0 ||
+                       PyModule_AddStringConstant(m, "header_id", KVZ_HEADER_ID) != 0)) {
     Py_DECREF(m);
     return nullptr;
   }

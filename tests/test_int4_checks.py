@@ -281,3 +281,43 @@ def test_kernels_that_start_early_read_by_ordinary_loads():
     assert len(early) >= 6
     for p in early:
         assert not re.search(r"__ldg|\.nc\b|__restrict__", re.sub(r"//[^\n]*", "", text[p])), p
+
+
+# ---------------------------------------------------------------------------
+# The host module
+# ---------------------------------------------------------------------------
+def test_a_host_module_that_cannot_be_compiled_leaves_none_behind(tmp_path, monkeypatch):
+    # the module of an earlier build, of an earlier header, must not be imported in its place
+    from query_agnostic_kv_kvz_b200 import build
+    old = [tmp_path / os.path.basename(build.FAST), tmp_path / "_kvz_fast.so"]
+    for p in old:
+        p.write_bytes(b"an earlier build")
+    stamp = tmp_path / "stamp"
+    stamp.write_text("x")
+    monkeypatch.setattr(build, "FAST", str(old[0]))
+    monkeypatch.setattr(build, "FAST_STAMP", str(stamp))
+    monkeypatch.setenv("CXX", "false")
+    assert build.build_fast() is False
+    assert not any(p.exists() for p in old) and not stamp.exists()
+
+
+@pytest.mark.parametrize("wrong", ["torch_version", "header_id"])
+def test_a_host_module_of_another_build_is_not_bound(monkeypatch, wrong):
+    from types import SimpleNamespace
+
+    from query_agnostic_kv_kvz_b200 import build
+
+    def bind(*a):
+        raise AssertionError("bound")
+    fake = dict(torch_version=torch.__version__, header_id=build.header_id(), bind=bind)
+    fake[wrong] = "another"
+    kvz.lib()
+    monkeypatch.setattr(kvz, "_kvz_fast", SimpleNamespace(**fake), raising=False)
+    monkeypatch.setattr(kvz, "_fast", None)
+    kvz._load_fast()
+    assert kvz._fast is None
+    del fake[wrong]                                   # a module of before it said so
+    monkeypatch.setattr(kvz, "_kvz_fast", SimpleNamespace(**{"torch_version": torch.__version__, **fake}))
+    if wrong == "header_id":
+        kvz._load_fast()
+        assert kvz._fast is None
