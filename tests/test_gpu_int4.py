@@ -764,6 +764,25 @@ def test_short_and_long_way_on_the_host_agree(monkeypatch):
         assert torch.equal(a.view(torch.uint8) if a.is_contiguous() else a, b.view(torch.uint8) if b.is_contiguous() else b)
 
 
+@pytest.mark.parametrize("short", [True, False])
+def test_new_outputs_are_filled_where_torch_fills_them(short, monkeypatch):
+    # torch.empty fills with NaN under deterministic algorithms; rows that no call writes show it
+    if not short:
+        monkeypatch.setattr(kvz, "_fast", None)
+    cache, pages, n, k, v = filled([3, 3], 64, 16, 7)
+    q = rand((2, 2, 3, 64), 8)
+    torch.use_deterministic_algorithms(True)
+    try:
+        got, q_out = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros_like(n), 16, q=q,
+                                         n_new=torch.tensor([1, 2], dtype=torch.int32, device="cuda"))
+        K, V = kvz.kvz_expand_int4(cache, pages, got, offsets_of([1, 2]), 16, out_rows=5)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert torch.equal(q_out[0, :, 0], q[0, :, 0]) and torch.equal(q_out[1, :, :2], q[1, :, :2])
+    assert bool(torch.isnan(q_out[0, :, 1:]).all()) and bool(torch.isnan(q_out[1, :, 2:]).all())
+    assert bool(torch.isnan(K[3:]).all()) and bool(torch.isnan(V[3:]).all()) and bool(torch.isfinite(K[:3]).all())
+
+
 # ---------------------------------------------------------------------------
 # Streams, graphs, and the whole path
 # ---------------------------------------------------------------------------
