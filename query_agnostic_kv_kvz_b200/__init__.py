@@ -1053,7 +1053,7 @@ def _cache4(fn, cache, pages, page_size, d=None):
     _vec(fn, "pages", pages, _i32t, 0, required=True)
     if page_size < 16 or page_size > 1024 or page_size & 15:
         raise ValueError("%s: page_size must be a multiple of 16 in [16, 1024], got %r" % (fn, page_size))
-    width = cache.shape[-1]
+    width = cache.shape[-1] if cache.dim() == 2 else 0
     if d is None:
         d = 128 if width == page_size * 144 else 64
     if d != 64 and d != 128:

@@ -764,6 +764,81 @@ def test_short_and_long_way_on_the_host_agree(monkeypatch):
         assert torch.equal(a.view(torch.uint8) if a.is_contiguous() else a, b.view(torch.uint8) if b.is_contiguous() else b)
 
 
+def _spaced(t):
+    w = torch.zeros((*t.shape[:-1], t.shape[-1] + 8), dtype=t.dtype, device=t.device)
+    w[..., : t.shape[-1]] = t
+    return w[..., : t.shape[-1]]
+
+
+def _shifted(t):
+    w = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+    w[1:] = t.reshape(-1)
+    return w[1:].view(t.shape)
+
+
+OTHER_TYPE = {torch.bfloat16: torch.float32, torch.float32: torch.bfloat16, torch.int32: torch.int64,
+              torch.int64: torch.int32, torch.uint8: torch.int32}
+OTHER_TENSORS = {
+    "None": lambda t: None, "on the host": lambda t: t.cpu(), "type": lambda t: t.to(OTHER_TYPE[t.dtype]),
+    "list": lambda t: t.tolist(), "number": lambda t: 3, "one less": lambda t: t[:-1].contiguous(),
+    "narrower": lambda t: t[..., :-1].contiguous(), "twice": lambda t: torch.cat([t, t]), "one more dim": lambda t: t[None],
+    "flat": lambda t: t.reshape(-1), "empty": lambda t: t[:0], "rows apart": _spaced, "odd address": _shifted,
+    "transposed": lambda t: t.transpose(0, -1), "expanded": lambda t: t[:1].expand(t.shape),
+    "no dim": lambda t: t.reshape(-1)[0], "parameter": lambda t: torch.nn.Parameter(t) if t.is_floating_point() else t,
+}
+OTHER_VALUES = {"page_size": [0, 8, 24, 32, 48, 2048, -16, 16.0, "16", True, 1 << 40],
+                "scale": [None, 1, 0.0, -1.0, float("nan"), float("inf"), 1e-50, 1e50, True],
+                "interleaved": [True, 1, 0, None, "x", 2], "inverse": [True, 1, 0, None, 2],
+                "out_rows": [None, 0, -1, 39, 100, 40.0, True]}
+
+
+@pytest.mark.parametrize("name", ["append", "decode", "expand", "compact", "rotary"])
+def test_every_argument_changed_both_ways_on_the_host(name, monkeypatch):
+    # each tensor and value of a call changed in the usual ways: with and without the host module it is accepted with
+    # outputs of the same form, or refused by the same error
+    short = kvz._fast
+    assert short is not None, "csrc/fast_calls.cpp is not built"
+    B, T, G, d, page = 3, 2, 2, 64, 16
+    cache, pages, n, k, v = filled([20, 3, 17], d, page, 3)
+    pages = torch.cat([pages, torch.full_like(pages[:, :1], -1)], 1)
+    k, v, q, t = k[:, :T].contiguous(), v[:, :T].contiguous(), rand((B, G, T, d), 5), table(d, 90)
+    pos = torch.randint(0, 90, (B, T), dtype=torch.int32, device="cuda")
+    K, idx, off = rand((B, 40, d), 6), torch.arange(40, dtype=torch.int32, device="cuda"), offsets_of([20, 3, 17])
+    at = dict(cache=cache, pages=pages, counts=n, page_size=page)
+    f, base = {
+        "append": (kvz.kvz_append_int4, dict(k=k, v=v, positions=pos, table=t, interleaved=False, q=q, n_new=n // n,
+                                             q_out=torch.zeros_like(q), counts_out=torch.zeros_like(n), **at)),
+        "decode": (kvz.kvz_decode_int4, dict(q=q[:, :, 0].contiguous(), scale=0.125, out=torch.zeros((B, G, d), device="cuda"),
+                                             lse2=torch.zeros((B, G), device="cuda"),
+                                             workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"), **at)),
+        "expand": (kvz.kvz_expand_int4, dict(offsets=off, first=n - n, out_rows=40, **at)),
+        "compact": (kvz.kvz_compact_int4, dict(K=K, V=K, idx=idx, offsets=off, **at)),
+        "rotary": (kvz.kvz_rotary, dict(x=q, positions=pos, table=t, interleaved=False, inverse=False)),
+    }[name]
+    base["status"] = new_status()
+    c0 = cache.clone()
+
+    def outcome(kw):
+        try:
+            r = f(**kw)
+        except (ValueError, kvz.KvzError) as e:
+            return type(e), getattr(e, "code", None)
+        finally:
+            cache.copy_(c0)
+        return [x if x is None else (x.dtype, x.shape, x.stride()) for x in (r if isinstance(r, tuple) else (r,))]
+
+    assert isinstance(outcome(base), list)
+    for arg, val in base.items():
+        others = OTHER_VALUES[arg] if arg in OTHER_VALUES else [
+            change(val) for kind, change in OTHER_TENSORS.items()]
+        for i, x in enumerate(others):
+            kw = {**base, arg: x}
+            monkeypatch.setattr(kvz, "_fast", short)
+            a = outcome(kw)
+            monkeypatch.setattr(kvz, "_fast", None)
+            assert a == outcome(kw), (arg, i)
+
+
 @pytest.mark.parametrize("short", [True, False])
 def test_new_outputs_are_filled_where_torch_fills_them(short, monkeypatch):
     # torch.empty fills with NaN under deterministic algorithms; rows that no call writes show it

@@ -97,6 +97,8 @@ CASES = {
     "append: pages rank": append(pages=z(6, i32)),
     "append: cache of d = 128": append(cache=z((6, page * 144), u8)),
     "append: page size 0": append(ps=0),
+    "append: cache of no dimension": append(cache=z((), u8)),
+    "append: cache flat": append(cache=z(6 * pb, u8)),
     "append: too many rows": append(pages=z((B, (1 << 30) // page + 1), i32).expand(B, -1)),
     "append: CPU": append(),
     "expand: no rows given": lambda: kvz.kvz_expand_int4(cache, pages, cnt, off, page),
