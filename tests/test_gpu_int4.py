@@ -380,6 +380,16 @@ def test_decode_many_heads():
     check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
 
 
+def test_decode_many_heads_in_shares():
+    # a table wide enough for shares of equal work: more heads than counts kept on chip, many empty, every CTA's share
+    # spans several
+    counts = [(n * 7) % 40 if n % 3 else 0 for n in range(1500)]
+    cache, pages, n, _, _ = filled(counts, 64, 16, 12)
+    pages = wide(pages, 16)
+    assert kvz.kvz_decode_int4_workspace_size(1500, 2, pages.shape[1] * 16, 64) > 0
+    check_decode(rand((1500, 2, 64), 2), cache, pages, n, 16, 0.125)
+
+
 def test_decode_many_heads_and_a_long_one():
     # the same with a head long enough for shares of equal work: most CTAs begin, hold and end several heads
     counts = [(n * 7) % 40 if n % 3 else 0 for n in range(1500)]
@@ -875,6 +885,35 @@ def test_streams():
         s.synchronize()
     for o, l2 in outs:
         assert torch.equal(o, ref[0]) and torch.equal(l2, ref[1])
+
+
+def test_streams_with_scratch():
+    # the same with shares of equal work, whose scratch every call allocates: each stream asks other questions of
+    # another cache, so scratch that two calls shared would show
+    page, d, G = 64, 128, 4
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    sets = []
+    for i in range(len(sides)):
+        cache, pages, n, _, _ = filled([9000, 40 + i, 15000 - 999 * i], d, page, 38 + i)
+        pages = wide(pages, page)
+        assert kvz.kvz_decode_int4_workspace_size(3, G, pages.shape[1] * page, d) > 0
+        q = [rand((3, G, d), 500 + 10 * i + j) for j in range(8)]
+        sets.append((cache, pages, n, q, [kvz.kvz_decode_int4(x, cache, pages, n, page) for x in q]))
+    torch.cuda.synchronize()
+    outs = [[] for _ in sides]
+    for j in range(8):
+        for i, s in enumerate(sides):
+            cache, pages, n, q, _ = sets[i]
+            if j % 2:
+                outs[i].append(kvz.kvz_decode_int4(q[j], cache, pages, n, page, stream=s))
+            else:
+                with torch.cuda.stream(s):
+                    outs[i].append(kvz.kvz_decode_int4(q[j], cache, pages, n, page))
+    for s in sides:
+        s.synchronize()
+    for i in range(len(sides)):
+        for got, ref in zip(outs[i], sets[i][4]):
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
 def test_decoding_in_graphs_that_share_a_workspace():
