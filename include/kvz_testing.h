@@ -42,23 +42,27 @@ kvz_status kvz_testing_compact_in_place_withhold(void* K, void* V, int64_t B, in
 /*                                                                          */
 /* Same arguments, layout and result as kvz_decode_int4, except that         */
 /*   - every wait for rows gives up after wait_ns nanoseconds                */
-/*     (kvz_decode_int4: 1 s), and                                           */
+/*     (kvz_decode_int4: 1 s),                                               */
 /*   - the first rows of head hold_head that warp 0 of CTA hold_cta (-1:     */
-/*     every CTA that reads the head) would bring in are never asked for.    */
+/*     every CTA that reads the head) would bring in are never asked for     */
+/*     (hold_head -1: all are), and                                          */
+/*   - clusters have at most max_cluster CTAs, as on a part of a GPU that    */
+/*     has no room for wider ones.                                           */
 /* That warp's wait runs out: the kernel sets KVZ_ERR_TIMEOUT in d_status    */
 /* and returns, and the heads that such a CTA had still to read are NaN in   */
 /* out and lse2 (where other CTAs read a part of one, too).  Heads that only */
 /* other CTAs read are as kvz_decode_int4 gives them.  The wait is a bounded */
 /* poll of an mbarrier in shared memory on %globaltimer; nothing traps.      */
-/* Limits: 1000 <= wait_ns <= 1e9; 0 <= hold_head < B; hold_cta >= -1.       */
+/* Limits: 1000 <= wait_ns <= 1e9; -1 <= hold_head < B; hold_cta >= -1;      */
+/* max_cluster in {1, 2, 4, 8, 16}.                                          */
 /* Workspace: kvz_decode_int4_workspace_size, as there.                      */
 /* ------------------------------------------------------------------------ */
 kvz_status kvz_testing_decode_int4_withhold(const void* q, const void* cache, int64_t n_pages, int page_size,
                                             const int32_t* pages, int64_t max_pages, const int32_t* counts,
                                             int64_t B, int G, int d, float scale, float* out, float* lse2,
                                             void* workspace, size_t workspace_bytes, int64_t wait_ns,
-                                            int64_t hold_head, int64_t hold_cta, int32_t* d_status,
-                                            cudaStream_t stream);
+                                            int64_t hold_head, int64_t hold_cta, int max_cluster,
+                                            int32_t* d_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

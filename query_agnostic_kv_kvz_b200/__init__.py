@@ -103,7 +103,7 @@ _SIGS = {
     "kvz_decode_int4": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp,
                                _vp]),
     "kvz_testing_decode_int4_withhold": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _f32, _vp, _vp,
-                                                _vp, _sz, _i64, _i64, _i64, _vp, _vp]),
+                                                _vp, _sz, _i64, _i64, _i64, _i32, _vp, _vp]),
     "kvz_testing_compact_in_place_withhold": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _i64, _i64,
                                                      _i64, _vp, _vp]),
 }
@@ -1273,10 +1273,12 @@ def kvz_testing_compact_in_place_withhold(K, V, idx, counts, offsets, wait_ns: i
 
 
 def kvz_testing_decode_int4_withhold(q, cache, pages, counts, page_size: int, wait_ns: int, hold_head: int,
-                                     hold_cta: int = -1, out=None, lse2=None, workspace=None, status=None):
+                                     hold_cta: int = -1, max_cluster: int = 16, out=None, lse2=None, workspace=None,
+                                     status=None):
     """Test-only (include/kvz_testing.h): kvz_decode_int4 whose waits give up
     after ``wait_ns`` and in which the first rows of head ``hold_head`` never
-    arrive at warp 0 of CTA ``hold_cta`` (-1: of every CTA that reads it).
+    arrive at warp 0 of CTA ``hold_cta`` (-1: of every CTA that reads it;
+    ``hold_head`` -1: they all do), with clusters of at most ``max_cluster``.
     Returns (out, lse2); the heads such a CTA still had to read are NaN."""
     fn = "kvz_testing_decode_int4_withhold"
     _vec(fn, "q", q, _bf16, 0, required=True)
@@ -1300,5 +1302,5 @@ def kvz_testing_decode_int4_withhold(q, cache, pages, counts, page_size: int, wa
             q.data_ptr(), cache.data_ptr(), cache.shape[0], page_size, pages.data_ptr(), pages.shape[1],
             counts.data_ptr(), B, G, d, d ** -0.5, out.data_ptr(), lse2.data_ptr(),
             workspace.data_ptr() if workspace.numel() else None, workspace.numel(), int(wait_ns), int(hold_head),
-            int(hold_cta), _addr(status), _raw(dev)))
+            int(hold_cta), int(max_cluster), _addr(status), _raw(dev)))
     return out, lse2

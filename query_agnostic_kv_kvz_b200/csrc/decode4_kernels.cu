@@ -49,6 +49,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "kvz.h"
@@ -989,17 +990,50 @@ __global__ void __launch_bounds__(kD4Threads) merge_int4_kernel(Dec4Args p) {
   }
 }
 
+// The widest cluster of at most `want` CTAs (a power of two) that the device
+// has room for: a process may be limited to a part of its SMs, where 16 CTAs
+// of their own find no place.  Asked once per device, size and shared memory.
+template <auto Kernel>
+int widest_cluster(int want, int smem, bool alone) {
+  static std::atomic<uint8_t> known[64][2][5];                // [device][alone][log2 want]
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return want;
+  std::atomic<uint8_t>& answer = known[dev][alone ? 1 : 0][31 - __builtin_clz(static_cast<unsigned>(want))];
+  int c = answer.load(std::memory_order_relaxed);
+  if (c > 0) return c;
+  for (c = want; c > 1; c /= 2) {
+    if (c > 8 && wide_clusters_once<Kernel>() != cudaSuccess) continue;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(c);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(c));
+    cfg.blockDim = dim3(kD4Threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) == cudaSuccess && n > 0) break;
+  }
+  cudaGetLastError();                                         // (a size that was refused is not this call's error)
+  answer.store(static_cast<uint8_t>(c), std::memory_order_relaxed);
+  return c;
+}
+
 template <int D, bool TEST>
 cudaError_t launch_decode4(const Dec4Args& a, cudaStream_t stream) {
   const Decode4Form form = decode4_form(a.B, a.cap);
   if (form.cluster > 0) {
     constexpr int kAlone = 115 * 1024;                        // of an SM's 228 KB: one CTA
     static_assert(D4<D>::SMEM <= kAlone, "");
-    cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D, TEST>>(kAlone);
-    if (e == cudaSuccess && form.cluster > 8) e = wide_clusters_once<decode_int4_cluster_kernel<D, TEST>>();
+    const cudaError_t e = smem_limit_once<decode_int4_cluster_kernel<D, TEST>>(kAlone);
     if (e != cudaSuccess) return e;
-    return launch_after(decode_int4_cluster_kernel<D, TEST>, dim3(static_cast<unsigned>(a.B * form.cluster)), dim3(kD4Threads),
-                        form.alone ? kAlone : D4<D>::SMEM, stream, form.cluster, a);
+    const int smem = form.alone ? kAlone : D4<D>::SMEM;
+    const int c = widest_cluster<decode_int4_cluster_kernel<D, TEST>>(
+        TEST && a.max_cluster < form.cluster ? a.max_cluster : form.cluster, smem, form.alone);
+    return launch_after(decode_int4_cluster_kernel<D, TEST>, dim3(static_cast<unsigned>(a.B * c)), dim3(kD4Threads), smem,
+                        stream, c, a);
   }
   cudaError_t e = smem_limit_once<decode_int4_kernel<D, TEST>>(D4<D>::SMEM);
   if (e != cudaSuccess) return e;

@@ -52,7 +52,7 @@ kvz_status check_rotation(const int32_t* positions, int64_t pos_sb, const float*
 kvz_status decode_int4(const void* q, const void* cache, int64_t n_pages, int page_size, const int32_t* pages,
                        int64_t max_pages, const int32_t* counts, int64_t B, int G, int d, float scale, float* out,
                        float* lse2, void* workspace, size_t workspace_bytes, uint64_t wait_ns, int64_t hold_head,
-                       int64_t hold_cta, int32_t* d_status, cudaStream_t stream) {
+                       int64_t hold_cta, int max_cluster, int32_t* d_status, cudaStream_t stream) {
   if (q == nullptr || counts == nullptr || out == nullptr) return KVZ_ERR_INVALID_ARG;
   kvz::Dec4Args a{};
   const kvz_status st = check_pages(cache, n_pages, page_size, pages, max_pages, B, d, &a.pg);
@@ -76,7 +76,7 @@ kvz_status decode_int4(const void* q, const void* cache, int64_t n_pages, int pa
   w += up256(2 * kvz::kD4Workers * 8 * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(w);
   a.status = d_status;
-  a.wait_ns = wait_ns, a.hold_head = hold_head, a.hold_cta = hold_cta;
+  a.wait_ns = wait_ns, a.hold_head = hold_head, a.hold_cta = hold_cta, a.max_cluster = max_cluster;
   return kvz::launch_decode_int4(d, a, stream) == cudaSuccess ? KVZ_OK : KVZ_ERR_CUDA;
 }
 
@@ -206,18 +206,20 @@ kvz_status kvz_decode_int4(const void* q, const void* cache, int64_t n_pages, in
                            float* lse2, void* workspace, size_t workspace_bytes, int32_t* d_status,
                            cudaStream_t stream) {
   return decode_int4(q, cache, n_pages, page_size, pages, max_pages, counts, B, G, d, scale, out, lse2, workspace,
-                     workspace_bytes, 0, -1, -1, d_status, stream);
+                     workspace_bytes, 0, -1, -1, 16, d_status, stream);
 }
 
 kvz_status kvz_testing_decode_int4_withhold(const void* q, const void* cache, int64_t n_pages, int page_size,
                                             const int32_t* pages, int64_t max_pages, const int32_t* counts, int64_t B,
                                             int G, int d, float scale, float* out, float* lse2, void* workspace,
                                             size_t workspace_bytes, int64_t wait_ns, int64_t hold_head,
-                                            int64_t hold_cta, int32_t* d_status, cudaStream_t stream) {
-  if (wait_ns < 1000 || wait_ns > 1000000000 || hold_head < 0 || hold_head >= B || hold_cta < -1)
+                                            int64_t hold_cta, int max_cluster, int32_t* d_status,
+                                            cudaStream_t stream) {
+  if (wait_ns < 1000 || wait_ns > 1000000000 || hold_head < -1 || hold_head >= B || hold_cta < -1)
     return KVZ_ERR_INVALID_ARG;
+  if (max_cluster < 1 || max_cluster > 16 || (max_cluster & (max_cluster - 1)) != 0) return KVZ_ERR_INVALID_ARG;
   return decode_int4(q, cache, n_pages, page_size, pages, max_pages, counts, B, G, d, scale, out, lse2, workspace,
-                     workspace_bytes, static_cast<uint64_t>(wait_ns), hold_head, hold_cta, d_status, stream);
+                     workspace_bytes, static_cast<uint64_t>(wait_ns), hold_head, hold_cta, max_cluster, d_status, stream);
 }
 
 }  // extern "C"

@@ -249,6 +249,7 @@ struct Dec4Args {
   // the test entry point's only: its waits' limit, and the head and CTA (-1: any) whose first stage stays away
   uint64_t wait_ns = 0;
   int64_t hold_head = -1, hold_cta = -1;
+  int max_cluster = 16;                     // and the widest cluster it may take
 };
 // The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
 // table holds `cap` rows, or 0 for shares of equal work; `alone`: each on an SM

@@ -368,6 +368,31 @@ def test_decode_by_clusters_of_every_size(B, d, G):
     check_decode(rand((B, G, d), B), cache, pages, n, 32, d ** -0.5)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("widest", [1, 2, 4, 8, 16])
+def test_decode_by_narrower_clusters_than_chosen(widest, d):
+    # a part of a GPU that has no room for clusters of 16: the heads that would have them, up to their longest, by fewer
+    # CTAs, whose warps then look up their pages several times
+    counts, page, G = [20480, 1, 0, 12345, 700], 32, 4
+    cache, pages, n, _, _ = filled([c - 1 if c == 20480 else c for c in counts], d, page, 12)
+    assert kvz.kvz_decode_int4_workspace_size(5, G, pages.shape[1] * page, d) == 0
+    q, st = rand((5, G, d), 13), new_status()
+    ref, rl = check_decode(q, cache, pages, n, page, d ** -0.5)
+    out, lse2 = kvz.kvz_testing_decode_int4_withhold(q, cache, pages, n, page, 1_000_000_000, -1, max_cluster=widest,
+                                                     status=st)
+    assert st.item() == 0
+    if widest == 16:
+        assert torch.equal(out, ref) and torch.equal(lse2, rl)
+    ch, ph, cn, qd = cache.cpu().numpy(), pages.cpu().numpy(), n.cpu().numpy(), f64(q)
+    for b in range(5):
+        if cn[b] == 0:
+            assert bool((out[b] == 0).all()) and bool(torch.isneginf(lse2[b]).all())
+            continue
+        K, V = o4.read_head(ch, ph[b], page, d, int(cn[b]))
+        want, tol = o4.decode_bound_by_group(qd[b], K, V, d ** -0.5)
+        assert np.all(np.abs(out[b].cpu().double().numpy() - want) <= tol)
+
+
 def test_decode_one_long_head():
     cache, pages, n, _, _ = filled([100003], 128, 128, 11)    # every CTA reads a part of it
     check_decode(rand((1, 5, 128), 1), cache, pages, n, 128, 0.088)

@@ -168,7 +168,7 @@ def test_attention_by_clusters_whose_wait_expires(B, head):
 
 def test_attention_withhold_arguments_are_checked():
     cache, pages, n, q = _four_bit([40, 40], 64, 32, 1)
-    for wait_ns, hb, hc in [(10, 0, 0), (2_000_000_000, 0, 0), (1_000_000, 2, 0), (1_000_000, -1, 0), (1_000_000, 0, -2)]:
+    for wait_ns, hb, hc in [(10, 0, 0), (2_000_000_000, 0, 0), (1_000_000, 2, 0), (1_000_000, -2, 0), (1_000_000, 0, -2)]:
         with pytest.raises(kvz.KvzError) as e:
             kvz.kvz_testing_decode_int4_withhold(q, cache, pages, n, 32, wait_ns, hb, hc)
         assert e.value.code == 1
