@@ -462,8 +462,9 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /*   k is turned as by kvz_rotary first (bf16, then quantised), and so is q: */
 /*   q_out [B][G][T][d] (q may be NULL, q_out then too; without positions q  */
 /*   is only laid out).  Rows of q_out at and past n_new[b] are not written. */
-/*   counts_out[b] = counts[b] + n_new[b] (optional; must not overlap        */
-/*   counts).  B * (T + 2) <= 2^28, B * G * T < 2^31.                        */
+/*   counts_out[b] = counts[b] + n_new[b] (optional).  counts_out must not   */
+/*   overlap counts, n_new or positions, nor q_out k, v or q.                */
+/*   B * (T + 2) <= 2^28, B * G * T < 2^31.                                  */
 /* kvz_expand_int4: rows first[b] (NULL: 0) .. counts[b] - 1 of head b, as   */
 /*   bf16(s * code + m), to rows offsets[b], offsets[b] + 1, ... of K_out,   */
 /*   V_out [n_rows][d].  offsets [B + 1] must ascend and leave each head its */

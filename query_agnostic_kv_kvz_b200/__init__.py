@@ -1131,9 +1131,11 @@ def kvz_append_int4(k, v, cache, pages, counts, page_size: int, positions=None, 
     if counts_out is not None:
         _vec(fn, "counts_out", counts_out, _i32t, B)
         _apart(fn, "counts", counts, "counts_out", counts_out)
+        _apart(fn, "n_new", n_new, "counts_out", counts_out)
     pos_sb = n_pos = rot = 0
     if positions is not None or table is not None:
         pos_sb, n_pos, rot = _rotation(fn, positions, table, B, T)
+        _apart(fn, "positions", positions, "counts_out", counts_out)
     G, qs = 1, (0, 0, 0)
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
@@ -1142,7 +1144,8 @@ def kvz_append_int4(k, v, cache, pages, counts, page_size: int, positions=None, 
         qs = _rows_view(fn, "q", q, (B, G, T, d))
         if q_out is not None:
             _dense(fn, "q_out", q_out, _bf16, (B, G, T, d))
-            _apart(fn, "q", q, "q_out", q_out)
+            for name, x in (("q", q), ("k", k), ("v", v)):
+                _apart(fn, name, x, "q_out", q_out)
     elif q_out is not None:
         raise ValueError("%s: q_out needs q" % fn)
     _vec(fn, "status", status, _i32t, 1)

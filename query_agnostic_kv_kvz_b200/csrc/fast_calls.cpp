@@ -262,7 +262,11 @@ PyObject* append(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Tensor* n_new = a.dense(v[11], at::kInt, B, true);
     const at::Tensor* n_out = a.dense(v[12], at::kInt, B, true);
     const at::Tensor* status = a.dense(v[13], at::kInt, 1, true);
-    if (!a.current() || (n_out != nullptr && same_memory(*n_out, *counts))) return none();
+    if (!a.current()) return none();
+    if (n_out != nullptr && (same_memory(*n_out, *counts) || (n_new != nullptr && same_memory(*n_out, *n_new)) ||
+                             (t.pos != nullptr && same_memory(*n_out, *t.pos))))
+      return none();
+    if (q_given != nullptr && (same_memory(*q_given, *k) || same_memory(*q_given, *x))) return none();
     at::Tensor n_empty;
     if (n_out == nullptr) n_empty = a.empty({B}, at::kInt);
     at::Tensor q_new;

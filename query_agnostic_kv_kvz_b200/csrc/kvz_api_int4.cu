@@ -183,7 +183,9 @@ kvz_status kvz_append_int4(const void* k, int64_t k_sb, int64_t k_st, const void
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(counts, 4) ||
       !aligned(n_new, 4) || !aligned(counts_out, 4))
     return KVZ_ERR_ALIGNMENT;
-  if (counts_out == counts) return KVZ_ERR_INVALID_ARG;       // every warp of a head reads its old count
+  // every warp of a head reads its old count, its new rows' number and their positions
+  if (counts_out != nullptr && (counts_out == counts || counts_out == n_new || counts_out == positions))
+    return KVZ_ERR_INVALID_ARG;
   a.k = static_cast<const uint16_t*>(k), a.k_sb = k_sb, a.k_st = k_st;
   a.v = static_cast<const uint16_t*>(v), a.v_sb = v_sb, a.v_st = v_st;
   a.q = static_cast<const uint16_t*>(q), a.q_sb = q_sb, a.q_sg = q_sg, a.q_st = q_st;

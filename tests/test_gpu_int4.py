@@ -722,6 +722,21 @@ def test_append_refusals_on_the_device():
     assert st.item() == 1 and out_n.tolist() == [30] * 4 and torch.equal(cache, c1)
 
 
+def test_append_refuses_outputs_over_what_it_reads(monkeypatch):
+    cache, pages, n, k, v = filled([30, 30], 64, 16, 35)
+    k, v, q = k[:, :2], v[:, :2], rand((2, 3, 2, 64), 36)
+    pos, t, c0 = torch.zeros((2, 2), dtype=torch.int32, device="cuda"), table(64, 8), cache.clone()
+    new = torch.ones_like(n)
+    for short in (kvz._fast, None):
+        monkeypatch.setattr(kvz, "_fast", short)
+        for kw in (dict(n_new=new, counts_out=new), dict(positions=pos, table=t, counts_out=pos.view(-1)),
+                   dict(k=q[:, 0], q_out=q), dict(v=q[:, 0], q_out=q)):
+            with pytest.raises(ValueError):
+                kvz.kvz_append_int4(**{**dict(k=k, v=v, cache=cache, pages=pages, counts=n, page_size=16,
+                                              q=rand((2, 3, 2, 64), 37)), **kw})
+    assert torch.equal(cache, c0)
+
+
 def test_compact_reports_bad_idx_and_counts():
     B, n_c, d, page = 2, 100, 64, 16
     K, V = rand((B, n_c, d), 36), rand((B, n_c, d), 37)

@@ -84,6 +84,10 @@ CASES = {
     "append: counts dtype": append(counts=z(B, i64)),
     "append: no counts": append(counts=None),
     "append: counts in place": append(counts_out=cnt),
+    "append: counts over n_new": (lambda m: append(n_new=m, counts_out=m))(z(B, i32)),
+    "append: counts over positions": (lambda m: append(positions=m, table=tab, counts_out=m.view(-1)))(z((B, T), i32)),
+    "append: q_out over k": (lambda m: append(k=m[:, 0], q=x4, q_out=m))(z((B, G, T, d), bf16)),
+    "append: q_out over v": (lambda m: append(v=m[:, 1], q=x4, q_out=m))(z((B, G, T, d), bf16)),
     "append: positions without table": append(positions=pos),
     "append: table without positions": append(table=tab),
     "append: q heads": append(q=z((B + 1, G, T, d), bf16)),
@@ -205,7 +209,7 @@ def test_c_compact_refuses(lib, kw, code):
     (dict(T=1 << 20, B=60000), INVALID), (dict(pos=None), INVALID), (dict(table=None), INVALID),
     (dict(rot=8), UNSUPPORTED), (dict(il=3), INVALID), (dict(k_st=12), ALIGNMENT), (dict(v_sb=-8), ALIGNMENT),
     (dict(q_sg=1), ALIGNMENT), (dict(k=P + 4), ALIGNMENT), (dict(q_out=P + 8), ALIGNMENT), (dict(n_new=P + 1), ALIGNMENT),
-    (dict(counts_out=P), INVALID)])
+    (dict(counts_out=P), INVALID), (dict(n_new=2 * P), INVALID), (dict(pos=2 * P), INVALID)])
 def test_c_append_refuses(lib, kw, code):
     a = dict(k=P, k_sb=64, k_st=64, v=P, v_sb=64, v_st=64, q=P, q_sb=64, q_sg=64, q_st=64, q_out=2 * P, B=1, G=2, T=3,
              d=64, pos=P, pos_sb=0, table=P, n_pos=9, rot=64, il=0, **PAGES, counts=P, n_new=None, counts_out=2 * P,
