@@ -88,7 +88,7 @@ constexpr float kD4Out = 0x1p-16f;
 // largest is between 2^10 and 2^11, and it grows again as weights shrink under
 // a reference that moves.
 constexpr float kD4WeightTop = 32768.0f;
-constexpr float kD4MulTop = 0x1p110f;                         // where the power begins
+constexpr float kD4MulTop = 0x1p126f;                         // where the power begins
 __device__ __forceinline__ uint32_t field(float x) { return __float_as_uint(x) >> 23; }
 __device__ __forceinline__ float power(uint32_t field) { return __uint_as_float(field << 23); }
 
@@ -160,9 +160,9 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// w less the fp16 in the low (high) half of h, exact where h is w rounded; s * f for a
-// bf16 s in the low half of its word and a power of two f; and (s * 8 + m) kD4Out for
-// the m in its high half.  Mixed instructions, where widening first would take another.
+// w less the fp16 in the low (high) half of h, exact where h is w rounded; s kD4Out for
+// the bf16 s in the low half of its word; and (s * 8 + m) kD4Out for the m in its high
+// half.  Mixed instructions, where widening first would take another.
 __device__ __forceinline__ float less_lo(float w, uint32_t h) {
   float d;
   asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, l, m, %2;}" : "=f"(d) : "r"(h), "f"(w));
@@ -173,10 +173,11 @@ __device__ __forceinline__ float less_hi(float w, uint32_t h) {
   asm("{.reg .b16 l, h, m; mov.b32 {l, h}, %1; mov.b16 m, 0xBC00; fma.rn.f32.f16 %0, h, m, %2;}" : "=f"(d) : "r"(h), "f"(w));
   return d;
 }
-__device__ __forceinline__ float step_times(uint32_t s, float f) {
+__device__ __forceinline__ float step_out(uint32_t w) {
   float d;
-  asm("{.reg .b16 l, h, x, y; mov.b32 {l, h}, %1; mov.b32 {x, y}, %2; fma.rn.f32.bf16 %0, l, y, 0f00000000;}"
-      : "=f"(d) : "r"(s), "r"(__float_as_uint(f)));
+  asm("{.reg .b16 l, h, f; mov.b32 {l, h}, %1; mov.b16 f, 0x3780; fma.rn.f32.bf16 %0, l, f, 0f00000000;}"
+      : "=f"(d)
+      : "r"(w));
   return d;
 }
 __device__ __forceinline__ float middle(uint32_t w) {
@@ -412,7 +413,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
     }
   }
 
-  float o[S::MT][4];                                        // out^T tiles (dims x queries 2c, 2c + 1) times mul
+  float o[S::MT][4];                                        // out^T tiles (dims x queries 2c, 2c + 1), times mul
 #pragma unroll
   for (int t = 0; t < S::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
   float m_neg[2] = {INFINITY, INFINITY}, thr[2] = {-INFINITY, -INFINITY};   // -reference of queries 2c, 2c + 1
@@ -537,8 +538,9 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
           fma2(y0, y1, m8, m8, om[g][0], om[g][1]);
           om[g][0] = y0, om[g][1] = y1;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) w[g][k][h][e] = step_times(vp[k][h][g], mul[g][e]);
-          mul2(w[g][k][h][0], w[g][k][h][1], x[k][h][0], x[k][h][1]);
+          for (int e = 0; e < 2; ++e) w[g][k][h][e] = step_out(vp[k][h][g]);
+          mul2(w[g][k][h][0], w[g][k][h][1], x[k][h][0], x[k][h][1]);   // (not past 2^115; the power alone may be)
+          mul2(w[g][k][h][0], w[g][k][h][1], mul[g][0], mul[g][1]);
           wm = max3(wm, w[g][k][h][0], w[g][k][h][1]);
         }
     if (__any_sync(kFullMask, wm > kD4WeightTop)) {
@@ -550,7 +552,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) top = fmaxf(top, x[k][h][e] * bf_lo(vp[k][h][g]));
+            for (int h = 0; h < 2; ++h) top = fmaxf(top, x[k][h][e] * step_out(vp[k][h][g]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, sh));
           const uint32_t now = field(mul[g][e]), to = min(now, 264u - field(top));
@@ -562,7 +564,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              w[g][k][h][e] = x[k][h][e] * step_times(vp[k][h][g], mul[g][e]);
+              w[g][k][h][e] = x[k][h][e] * step_out(vp[k][h][g]) * mul[g][e];
         }
     }
 
@@ -629,7 +631,7 @@ __device__ __forceinline__ bool read_part(const Dec4Args& p, const Query4<D>& qu
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float* d0 = s_o + (warp * 8 + 2 * c + e) * D + 64 * g + 8 * r;
-      const float s_out = kD4Out * 0x1p9f * power(254u - field(mul[g][e]));
+      const float s_out = power(254u + 9u - field(mul[g][e]));   // 2^9 / mul
 #pragma unroll
       for (int wl = 0; wl < 2; ++wl) {
         const float(&x0)[4] = o[4 * g + 2 * wl], (&x1)[4] = o[4 * g + 2 * wl + 1];

@@ -493,6 +493,22 @@ def test_decode_of_the_largest_values(n):
             assert bool(torch.isfinite(out).all())
 
 
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 20, 2.0 ** 100])
+@pytest.mark.parametrize("d,n,at", [(64, 1, 0), (128, 40, 5), (128, 40, 39), (64, 3000, 2900)])
+def test_decode_of_zeros_beside_values_of_no_weight(n, d, at, size):
+    # V is 0 but for one row, whose logit is so far below that its weight is 0 in any precision: the output is 0
+    page, G = 32, 4
+    q = (4.0 + rand((1, G, d), 88).clamp(-1, 1)).bfloat16()
+    k, v = rand((1, n, d), 89), torch.zeros((1, n, d), dtype=torch.bfloat16, device="cuda")
+    if n > 1:
+        k[:, at], v[:, at] = -200.0, rand((d,), 90) * size
+    cache, pages = pool([n], d, page, 5)
+    cnt, _ = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros(1, dtype=torch.int32, device="cuda"), page)
+    for p in (pages, wide(pages, page)):
+        out, _ = kvz.kvz_decode_int4(q, cache, p, cnt, page)
+        assert bool((out == 0).all())
+
+
 SPREADS = {
     # what row j and group g of V are multiplied by
     "second group 2^-10": lambda n, NG: torch.tensor([1.0, 2.0 ** -10])[:NG].expand(n, NG),
