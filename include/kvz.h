@@ -474,7 +474,15 @@ kvz_status kvz_rotary(const void* x, int64_t x_sb, int64_t x_sg, int64_t x_st, i
 /*   out = 0, lse2 = -inf.  1 <= G <= 8.  Workspace:                         */
 /*   kvz_decode_int4_workspace_size(B, G, max_pages * page_size, d) bytes    */
 /*   (0 where heads are short: NULL then), 256-byte aligned; it needs no     */
-/*   initial value and is free again when the call has finished.             */
+/*   initial value and is free again when the call has finished.  Lengths    */
+/*   are on the device, so the width of the page table stands for the        */
+/*   longest: pass the columns in use (a dense [B][max_pages] of them) while */
+/*   all heads are short, and the call takes its quicker form for them (5.0  */
+/*   against 8.2 us for one head of 2,000 rows).                             */
+/*   Sums are float32 on values scaled by 2^-16, so V may reach the largest  */
+/*   that quantisation takes (values below 2^-100 lose bits to underflow).   */
+/*   q's entries are exact down to 2^-27 of the query's largest, and held to */
+/*   2^-35 of it below.                                                      */
 /*                                                                          */
 /* Device-detected errors (KVZ_ERR_INVALID_ARG in d_status): a count outside */
 /* [0, max_pages * page_size] (the head is left out), a page id outside      */

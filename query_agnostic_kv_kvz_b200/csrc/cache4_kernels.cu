@@ -5,9 +5,9 @@
 // All three move rows through registers.  HBM-bound at length: 4 d bytes of
 // bf16 and 9/8 d bytes of the cache per row; a layer's few thousand rows are a
 // chain of dependent loads (head, page, index, row) behind a launch.  At d =
-// 128, in chains of calls: 311,051 of 32 x 32,768 rows compacted in 38.9 us
-// (5.3 TB/s) and expanded in 37.4 us (5.5 TB/s); 8 heads of 2,457 rows 5.4 and
-// 4.7 us; 32 ragged prompts, 8,716 tokens with 4 query heads each, appended in
+// 128, in chains of calls: 311,051 of 32 x 32,768 rows compacted in 39.2 us
+// (5.2 TB/s) and expanded in 37.0 us (5.5 TB/s); 8 heads of 2,457 rows 5.8 and
+// 4.8 us; 32 ragged prompts, 8,716 tokens with 4 query heads each, appended in
 // 9.1 us (2.6 TB/s); one token for 128 heads in 2.2 us.
 #include <cuda_runtime.h>
 

@@ -3,10 +3,12 @@
 //   out[b, g] = sum_j softmax_j(scale * <q_g, k_j>) v_j,
 //   k_j = s_j code_j + m_j (and v_j alike) per group of 64 dims.
 //
-// The codes are whole numbers, exact in fp16, so both products run on them
-// (mma.sync m16n8k16: the G <= 8 queries are below the 64 rows of tcgen05,
-// whose operands would have to be widened into shared or tensor memory first)
-// and the scales are applied to what comes out:
+// The codes are whole numbers, exact in fp16, so both products run on them and
+// the scales are applied to what comes out.  Keys, and V's dims, are the rows
+// of the products and the G <= 8 queries their columns (mma.sync m16n8k16).
+// tcgen05 takes its rows from shared or tensor memory, so every code would
+// have to be widened there first, 2 bytes written and read for half a byte of
+// the cache; here it is widened in the register that it was loaded to.
 //   <q, k_j> = sum_groups s_j <q, code_j> + m_j sum(q)
 //   out = sum_groups sum_j (p_j s_j) (code_j - 8) + p_j (m_j + 8 s_j)
 // The low 11 bits of an fp16 number count its 2^-24s (subnormal numbers, and
@@ -25,16 +27,18 @@
 // held to 2^-24 of itself, as float32 holds it, and to 2^-35 of that largest.
 // So neither the other group's steps nor a row of large values that hardly
 // counts costs a group its bits.  (Three bf16 numbers, which need no power of
-// two: 87.4 us against 77.9 for the heads below; one power for all that a warp
+// two: 87.4 us against 77.4 for the heads below, at that time; one power for all that a warp
 // reads, which loses the smaller group's bits: 76.4.)
 //
 // Bytes: 9/8 d per row (144 at d = 128), against 4 d of a bf16 cache.  At HBM's
 // rate an SM would have to widen and multiply a row (both of K and V, all
-// queries) in 6 clocks.  What bounds it is issue: 64 heads of 32,768 rows at
-// d = 128, G = 5 (302 MB) take 76 us, 4.0 TB/s; the same loads without the
-// arithmetic take 55 us, the arithmetic without the loads 74.  A stage of 32
-// rows costs a warp 680 instructions: issue slots are 58% busy, the integer
-// pipe 42%, the tensor pipe (48 products) 34%.
+// queries) in 6 clocks.  What bounds it is instructions that wait for one
+// another: 64 heads of 32,768 rows at d = 128, G = 5 (302 MB) take 76.9 us, 3.9
+// TB/s, the same loads without the arithmetic 55.  A stage of 32 rows costs a
+// warp 694 instructions, which would be 5.4 clocks a row if every slot issued;
+// 58% do, with 3.7 warps to a scheduler of which 1.2 could issue on average.  A
+// warp waits 1.8 cycles per instruction for a fixed latency, 1.0 for a pipe.
+// The integer pipe is 43% busy, the tensor pipe (48 products) 32%.
 //
 // One CTA of 8 warps takes an equal share of the work of all heads, whatever
 // the heads' lengths (a share may end one head and begin others).  A warp
@@ -69,10 +73,16 @@ constexpr int kD4Threads = kD4Warps * 32;
 constexpr int kD4Stages = 2;
 constexpr int kD4MinBlocks = 2 * kD4Warps;                    // a CTA's share is at least a stage per warp
 // What beginning another head costs a CTA (its queries, the ring's switch, the
-// join of the warps), counted as blocks: 64 heads of 32,768 rows (d = 128, G =
-// 5) took 80.5 us with 0, 80.0 with 8, 79.1 with 16, 77.0 with 40, 78.3 with
-// 72; 96 heads of very uneven lengths, 5,001 rows in the mean (d = 64, G = 8),
-// 24.0, 23.6, 22.2, 19.9 and 20.5.
+// join of the warps), counted as blocks.  us with 0, 16, 24, 40 and 72 (the
+// least for every d, G, page size and spread of lengths that was measured):
+//   64 heads of 32,768 rows    d 128  G 5  pages 128   80.6  78.9  77.6  77.2  78.5
+//                              d 128  G 1         64   78.8  77.4  75.6  75.6  77.2
+//                              d 64   G 8         64   51.0  50.2  48.6  48.2  49.7
+//   96 uneven heads, 5,001     d 64   G 8         16   23.9  21.5  20.8  20.2  20.6
+//   rows in the mean           d 128  G 4         64   33.0  30.0  28.4  27.8  28.7
+//   40 uneven of 20,000        d 128  G 8         16   42.7  41.2  40.4  39.5  40.8
+//   500 uneven of 1,500        d 64   G 2        128   37.7  32.3  31.4  29.6  32.3
+//   12 uneven of 60,000        d 64   G 1         64   23.5  22.6  22.3  21.2  21.5
 constexpr int kD4HeadCost = 40;
 constexpr int kD4Counts = 1024;                               // head counts kept in shared memory
 constexpr float kD4Slack = 7.0f;                              // log2 by which a logit may pass the reference
@@ -824,7 +834,7 @@ __device__ __forceinline__ void send(uint32_t at, const float2& v, uint32_t bar)
 // equal work gains.  Here the CTAs of a cluster read a head, its 32-row stages
 // in turn over all their warps.  Every CTA sends its state to the cluster's CTAs, each of
 // which joins a part of the dims: four dims in the lanes of a warp, a lane per
-// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 6.7 us in a
+// CTA that sent them.  8 heads of 2,457 rows (d = 128, G = 4): 6.6 us in a
 // chain of calls, of which the first 1.6 pass before the first rows are there
 // (count and page, then rows) and 1.2 in the join; a microsecond more when
 // every CTA fetched the others' states, two round trips and a barrier more.

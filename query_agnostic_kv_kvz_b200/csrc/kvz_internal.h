@@ -254,12 +254,13 @@ struct Dec4Args {
 // The cluster form (decode4_kernels.cu): the CTAs that read a head whose page
 // table holds `cap` rows, or 0 for shares of equal work; `alone`: each on an SM
 // of its own.  us at d = 128, G = 4, clusters against shares:
-//   1 head     2,000 rows 5.3 : 8.4    8,000 rows  7.5 :  8.7   16,000 rows 10.5 : 9.4
-//   6 heads               5.6 : 9.0                7.8 : 11.4               10.8 : 12.9
-//   12 heads              6.1 : 10.9              10.7 : 12.5               16.9 : 15.7
-//   20 heads              7.5 : 11.5   4,000 rows 10.6 : 12.5    6,000 rows 13.7 : 13.6
-//   32 heads              9.8 : 12.5   8,000 rows 16.9 : 18.2   12,000 rows 21.7 : 22.0
-//   96 heads             14.8 : 17.8   4,000 rows 23.8 : 23.5    6,000 rows 32.7 : 30.5
+//   1 head     2,000 rows 5.0 : 8.2    8,000 rows  7.3 :  8.7   16,000 rows 10.5 : 9.2
+//   6 heads               5.5 : 9.0                7.8 : 11.4               11.0 : 12.9
+//   12 heads              6.1 : 11.0              10.9 : 12.6               17.1 : 15.8
+//   20 heads              7.5 : 11.5   4,000 rows 10.7 : 12.6    6,000 rows 13.9 : 13.6
+//   32 heads             10.5 : 12.5   8,000 rows 18.6 : 18.4   12,000 rows 22.9 : 22.0
+//   64 heads             10.2 : 15.0   4,000 rows 15.2 : 18.9    6,000 rows 19.7 : 22.9
+//   96 heads             14.9 : 17.9   4,000 rows 24.1 : 23.7    6,000 rows 33.9 : 30.6
 // So clusters take the shorter heads.  Lengths are on the device, so the
 // table's width stands for the longest.  Few heads: the most CTAs up to 96
 // that have an SM each (more clusters do not fit the GPU's GPCs side by side:

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kRotThreads)
 // of one token, as two 16-byte vectors that hold whole pairs (so a row can be
 // turned in place), keeps their cosines and sines in registers and walks
 // `heads` rows of that token, four rows' loads in flight.  8 x 4 heads x 8,224
-// tokens x 128 from a token-major projection: 24.7 us = 5.6 TB/s in a chain of
+// tokens x 128 from a token-major projection: 24.1 us = 5.8 TB/s in a chain of
 // calls; 2 to 16 heads a thread, 2 or 4 rows in flight and 128 or 256 threads
 // all lie within 8% of it.
 template <int D, bool IL>
