@@ -547,6 +547,26 @@ def test_decode_of_values_of_very_different_size(n, name, d):
         assert np.all(off <= 1), (off.max(), np.abs(got - want).max())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("v_exp,q_exp", [(-95, 0), (-60, 0), (100, 0), (0, -24), (0, 40), (0, -90)])
+def test_decode_of_small_and_large_values_and_queries(v_exp, q_exp, d):
+    # all of V at one size; queries at another with keys at the inverse, so that the logits stay as they are, and half
+    # of the dims (a group, or every other 16) 2^-20 of the rest with keys 2^20 times as large
+    n, page, G = 700, 32, 3
+    half = (torch.arange(d, device="cuda") // (64 if d == 128 else 16)) % 2 == 1
+    skew = torch.where(half, 2.0 ** -20, 1.0).double()
+    q = (rand((1, G, d), 91).double() * skew * 2.0 ** q_exp).bfloat16()
+    k = (rand((1, n, d), 92).double() / skew * 2.0 ** -q_exp).bfloat16()
+    v = (rand((1, n, d), 93).double() * 2.0 ** v_exp).bfloat16()
+    cache, pages = pool([n], d, page, 5)
+    cnt, _ = kvz.kvz_append_int4(k, v, cache, pages, torch.zeros(1, dtype=torch.int32, device="cuda"), page)
+    K, V = o4.read_head(cache.cpu().numpy(), pages[0].cpu().numpy(), page, d, n)
+    want, tol = o4.decode_bound_by_group(f64(q)[0], K, V, d ** -0.5)
+    for p in (pages, wide(pages, page)):
+        got = kvz.kvz_decode_int4(q, cache, p, cnt, page)[0][0].cpu().double().numpy()
+        assert np.all(np.abs(got - want) <= tol), (np.abs(got - want) / tol).max()
+
+
 def test_decode_ignores_rows_past_the_end():
     # NaN scales behind the last row, in its block and on unused pages
     counts, d, page = [1, 18, 47], 128, 16
